@@ -157,6 +157,20 @@ def _pool(pages, page, fp8, g):
 
 
 def prepare(case, seed):
+    st = _inputs(case, seed)
+    if own and case["op"] != "rope":
+        # a serving loop keeps one workspace for its calls
+        from lightning_indexer_cross_b200 import ops
+        need = 256
+        if case["op"] == "decode":
+            need = ops.latent_decode_workspace_size(case["B"], case["Q"], case["H"], st["table"].shape[1] * case["page"])
+        if case["op"] == "sparse":
+            need = ops.latent_sparse_workspace_size(case["B"], case["H"], case["k"])
+        st["ws"] = ops.new_workspace(need, "cuda")
+    return st
+
+
+def _inputs(case, seed):
     g = torch.Generator(device="cuda").manual_seed(int(seed))
     op, st = case["op"], dict(case)
 
@@ -253,17 +267,20 @@ def run(st):
     op = st["op"]
     if own:
         from lightning_indexer_cross_b200 import ops
+        ws = st.get("ws")
         if op == "rope":
             return ops.rope(st["x"], st["pos"], st["freq"], rot_off=st["off"], layout=st["layout"],
                             mscale=st["mscale"])
         if op == "append":
-            ops.latent_append(st["kv"], st["slots"], st["cache"], pos=st["pos"], freq=st["freq"])
+            ops.latent_append(st["kv"], st["slots"], st["cache"], pos=st["pos"], freq=st["freq"], workspace=ws)
             return _views(st["cache"], st["fp8"])
         if op == "read":
-            return ops.latent_read(st["cache"], st["table"], st["cu"], st["out"])
+            return ops.latent_read(st["cache"], st["table"], st["cu"], st["out"], workspace=ws)
         if op == "decode":
-            return ops.latent_decode(st["q"], st["cache"], st["table"], st["lens"], sink=st["sink"], gate=st["gate"])
-        return ops.latent_sparse_decode(st["q"], st["cache"], st["slots"], sink=st["sink"], gate=st["gate"])
+            return ops.latent_decode(st["q"], st["cache"], st["table"], st["lens"], sink=st["sink"], gate=st["gate"],
+                                     workspace=ws)
+        return ops.latent_sparse_decode(st["q"], st["cache"], st["slots"], sink=st["sink"], gate=st["gate"],
+                                        workspace=ws)
     if op == "rope":
         x, off = st["x"], st["off"]
         y = _rotate(x[..., off:off + ROT].float(), st["pos"][:, None], st["freq"], st["layout"], st["mscale"])
@@ -307,7 +324,7 @@ def run(st):
 
 # ---------------------------------------------------------------- the definition in 64 bits
 def exact(case, seed):
-    st = prepare(case, seed)
+    st = _inputs(case, seed)
     op = case["op"]
 
     def turn(x, pos, layout, mscale):
