@@ -305,6 +305,128 @@ ic_status_t ic_decompress_gate(const void* o_latent, const void* wv_b, const voi
 size_t ic_decompress_gate_workspace_size(void);
 
 /* ---------------------------------------------------------------------------
+ * ic_rope -- rotary positions of a [T, H, D] tensor (Hy4-preview porting
+ * issue, "RoPE is interleaved" bullet, and the layouts and tables that other
+ * checkpoints of the family use).
+ *
+ * In every head, dims [rot_off, rot_off + rot_dim) rotate pairwise, the
+ * others are copied (nothing is copied when out is x):
+ *   a = pos[t] * freq[i],  c = mscale cos a,  s = mscale sin a
+ *   y_u = x_u c - x_v s,   y_v = x_u s + x_v c
+ *   IC_ROPE_INTERLEAVED: (u, v) = (2i, 2i + 1)
+ *   IC_ROPE_HALF:        (u, v) = (i, i + rot_dim / 2)      i < rot_dim / 2
+ * transpose != 0 applies the transposed map (s negated): it maps the gradient
+ * of y to that of x, and with mscale = 1 undoes the rotation.
+ *
+ *   x, out  bf16 or fp32 (dtype); element (t, h, d) at t * token_stride +
+ *           h * head_stride + d. out is x itself with the same strides, or
+ *           does not overlap it. Rows of out must not overlap one another.
+ *   pos     [T] int64 device, any sign.
+ *   freq    [rot_dim / 2] fp64 device: rad per position (long-context tables
+ *           scale it; 32 bits would lose 0.06 rad at position 10^6).
+ *   Supported: rot_dim even, <= 1024, D <= 65536, H <= 65535. The rotation is
+ *   32-bit, rounded once. No alignment beyond the element's is needed; 16-byte
+ *   aligned pointers, strides and parts run faster. No workspace.
+ * ------------------------------------------------------------------------- */
+typedef enum { IC_ROPE_INTERLEAVED = 0, IC_ROPE_HALF = 1 } ic_rope_layout_t;
+ic_status_t ic_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int64_t* pos,
+                    const double* freq, float mscale, ic_rope_layout_t layout, int transpose, ic_dtype_t dtype, int64_t T,
+                    int H, int D, int rot_off, int rot_dim, void* out, int64_t out_token_stride,
+                    int64_t out_head_stride, ic_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged latent cache: rows of 512 latent and 64 rotary dims in pages of
+ * page_size rows, page p at cache + p * page_stride BYTES, rows dense within
+ * a page. (The pages have no counterpart: how a serving engine keeps the
+ * latent rows of sequences that grow.)
+ *   IC_BF16:     a row is 576 bf16 values (1152 bytes).
+ *   IC_FP8_E4M3: a row is 656 bytes: 512 e4m3 codes, four fp32 scales (one for
+ *                each 128 dims), 64 bf16 rotary values.
+ *   Supported: page_size a multiple of 16; page_stride a multiple of 16 bytes
+ *   and at least a page's rows; num_pages < 2^31 - 65. cache 16-byte aligned.
+ *   Slot s of the cache is row s % page_size of page s / page_size. Row p of
+ *   sequence b is row p % page_size of page block_table[b, p / page_size];
+ *   block_table is int32 [B, table_width], table_stride elements a row.
+ *
+ * ic_latent_append writes T rows:
+ *   kv     [T, 576] bf16, kv_stride elements (a multiple of 8) between rows.
+ *   slots  [T] int64 device; -1: the token is skipped (padding). A slot
+ *          outside [-1, num_pages * page_size) is skipped and recorded as
+ *          IC_ERR_BAD_INDEX. Two tokens of one call must not name one slot.
+ *   pos, freq [32], mscale, layout: the rotary dims are rotated as by ic_rope;
+ *          pos and freq NULL: stored as given.
+ *   e4m3 rows: scale = 2^e, the least power of two >= max|y| / 448 over the
+ *   128 dims, e >= -100 (1 if all are zero); code = e4m3(y / scale), to
+ *   nearest even. An infinite y takes no part in the maximum and is stored as
+ *   +-448 scale, a NaN as NaN. A reader's code * scale is exact in bf16.
+ *
+ * ic_latent_read copies sequences back as bf16: rows cu_len[b] + p of out
+ * [R, 576] are row p of sequence b, p < cu_len[b + 1] - cu_len[b] (e4m3 rows
+ * as code * scale, rounded to bf16 where a foreign scale is no power of two).
+ *   cu_len [B + 1] int64 device, from 0 and not decreasing. Rows of out from
+ *   cu_len[B] on are left as they are. A position past the block table's row,
+ *   a page outside [0, num_pages) or cu_len[B] > R is recorded as
+ *   IC_ERR_BAD_INDEX (such rows of out are zeros; nothing is written past R).
+ *
+ * Workspaces: the matching *_workspace_size() bytes (status word).
+ * ------------------------------------------------------------------------- */
+ic_status_t ic_latent_append(const void* kv, int64_t kv_stride, const int64_t* slots, const int64_t* pos,
+                             const double* freq, float mscale, ic_rope_layout_t layout, int64_t T, ic_dtype_t cache_dtype,
+                             void* cache, int64_t num_pages, int page_size, int64_t page_stride, void* workspace,
+                             size_t ws_bytes, ic_stream_t stream);
+size_t ic_latent_append_workspace_size(void);
+ic_status_t ic_latent_read(const void* cache, ic_dtype_t cache_dtype, int64_t num_pages, int page_size,
+                           int64_t page_stride, const int32_t* block_table, int64_t table_stride, int table_width,
+                           const int64_t* cu_len, int B, void* out, int64_t R, void* workspace, size_t ws_bytes,
+                           ic_stream_t stream);
+size_t ic_latent_read_workspace_size(void);
+
+/* ---------------------------------------------------------------------------
+ * ic_latent_decode -- dense latent attention (absorbed form) of Q new tokens
+ * of each of B sequences over the paged cache: what a layer runs while a
+ * context is no longer than its top-k, and what dense layers run at any
+ * length. With z_p = sm_scale * q . row_p over the 576 dims of the rows that
+ * the token sees, out, lse, sink and gate are those of ic_sparse_mla_decode.
+ *
+ *   q      [B, Q, H, 576] bf16, rotary dims rotated.
+ *   lens   [B] int64 device: rows of each sequence, its Q new ones among them.
+ *          Token j sees positions p < lens[b] - (Q - 1 - j). lens[b] <= 0, or
+ *          a token that sees nothing: out = 0, lse = sink (-inf without one).
+ *          lens[b] > table_width * page_size is cut there, and recorded as
+ *          IC_ERR_BAD_INDEX, as is a negative one.
+ *   block_table  pages of each sequence; entries past a sequence's last row
+ *          are not read. A page outside [0, num_pages) is recorded as
+ *          IC_ERR_BAD_INDEX and its rows are not seen.
+ *   sink   [H] fp32 or NULL (none); gate [B, Q, H, 512] bf16 or NULL.
+ *   out    [B, Q, H, 512] bf16 or fp32; lse [B, Q, H] fp32 or NULL.
+ *   Rows of a page behind a sequence's end may hold anything. Rows that some
+ *   token of the sequence sees must be finite. The softmax's weights are
+ *   rounded to bf16 for the product with the values (fp32 outputs too).
+ *   The lengths and the table are read on the device.
+ *   workspace >= ic_latent_decode_workspace_size(B, Q, H, table_width *
+ *   page_size) bytes.
+ *
+ * ic_latent_sparse_decode -- ic_sparse_mla_decode over an e4m3 paged cache:
+ * query b attends to the k slots slots[b, :] (int32, -1 skipped, others
+ * outside [0, num_pages * page_size) skipped and recorded as
+ * IC_ERR_BAD_INDEX). For dense bf16 pages, ic_sparse_mla_decode itself takes
+ * the cache as one shared cache of num_pages * page_size rows.
+ *   num_pages * page_size < 2^31. q [B, H, 576], out [B, H, 512], lse [B, H].
+ *   workspace >= ic_latent_sparse_workspace_size(B, H, k) bytes.
+ * ------------------------------------------------------------------------- */
+ic_status_t ic_latent_decode(const void* q, const void* cache, ic_dtype_t cache_dtype, int64_t num_pages,
+                             int page_size, int64_t page_stride, const int32_t* block_table, int64_t table_stride,
+                             int table_width, const int64_t* lens, const float* sink, const void* gate, float sm_scale,
+                             int B, int Q, int H, ic_dtype_t out_dtype, void* out, float* lse, void* workspace,
+                             size_t ws_bytes, ic_stream_t stream);
+size_t ic_latent_decode_workspace_size(int B, int Q, int H, int64_t max_len);
+ic_status_t ic_latent_sparse_decode(const void* q, const void* cache, int64_t num_pages, int page_size,
+                                    int64_t page_stride, const int32_t* slots, int k, const float* sink,
+                                    const void* gate, float sm_scale, int B, int H, ic_dtype_t out_dtype, void* out,
+                                    float* lse, void* workspace, size_t ws_bytes, ic_stream_t stream);
+size_t ic_latent_sparse_workspace_size(int B, int H, int k);
+
+/* ---------------------------------------------------------------------------
  * Context-parallel decode: the N cached tokens split over G ranks, rank r
  * holding the contiguous shard [lo_r, hi_r) of the positions (Hy4 IndexCache
  * explainer, TL;DR and Jargon "Sparse attention": the indexer scores the

@@ -23,6 +23,9 @@ IC_BF16 = 0
 IC_FP8_E4M3 = 1
 IC_F32 = 2
 
+IC_ROPE_INTERLEAVED = 0
+IC_ROPE_HALF = 1
+
 # every symbol include/indexcache.h declares
 EXPORTED = [
     "ic_status_string",
@@ -50,6 +53,15 @@ EXPORTED = [
     "ic_cp_merge_topk",
     "ic_cp_combine",
     "ic_index_overlap",
+    "ic_rope",
+    "ic_latent_append",
+    "ic_latent_append_workspace_size",
+    "ic_latent_read",
+    "ic_latent_read_workspace_size",
+    "ic_latent_decode",
+    "ic_latent_decode_workspace_size",
+    "ic_latent_sparse_decode",
+    "ic_latent_sparse_workspace_size",
 ]
 
 
@@ -124,6 +136,19 @@ _cp_ws = _sig("ic_cp_workspace_size", _sz, [])
 _cp_merge = _sig("ic_cp_merge_topk", _i, [_p, _p, _i64, _i, _i, _i, _i, _i64, _i64, _p, _p, _p])
 _cp_combine = _sig("ic_cp_combine", _i, [_p, _i64, _p, _i64, _i, _i, _i, _p, _p, _i, _p, _p, _p])
 _overlap = _sig("ic_index_overlap", _i, [_p, _p, _i, _i, _i64, _p, _p])
+_rope = _sig("ic_rope", _i,
+             [_p, _i64, _i64, _p, _p, _f, _i, _i, _i, _i64, _i, _i, _i, _i, _p, _i64, _i64, _p])
+_lat_append = _sig("ic_latent_append", _i,
+                   [_p, _i64, _p, _p, _p, _f, _i, _i64, _i, _p, _i64, _i, _i64, _p, _sz, _p])
+_lat_append_ws = _sig("ic_latent_append_workspace_size", _sz, [])
+_lat_read = _sig("ic_latent_read", _i, [_p, _i, _i64, _i, _i64, _p, _i64, _i, _p, _i, _p, _i64, _p, _sz, _p])
+_lat_read_ws = _sig("ic_latent_read_workspace_size", _sz, [])
+_lat_decode = _sig("ic_latent_decode", _i,
+                   [_p, _p, _i, _i64, _i, _i64, _p, _i64, _i, _p, _p, _p, _f, _i, _i, _i, _i, _p, _p, _p, _sz, _p])
+_lat_decode_ws = _sig("ic_latent_decode_workspace_size", _sz, [_i, _i, _i, _i64])
+_lat_sparse = _sig("ic_latent_sparse_decode", _i,
+                   [_p, _p, _i64, _i, _i64, _p, _i, _p, _p, _f, _i, _i, _i, _p, _p, _p, _sz, _p])
+_lat_sparse_ws = _sig("ic_latent_sparse_workspace_size", _sz, [_i, _i, _i])
 _set_wait = _sig("ic_set_wait_limit_ns", None, [ctypes.c_uint64])
 _get_wait = _sig("ic_wait_limit_ns", ctypes.c_uint64, [])
 
@@ -243,6 +268,53 @@ def ic_cp_combine(part_out, out_stride, part_lse, lse_stride, G, B, H, sink, gat
 
 def ic_index_overlap(a, b, B, k, N, count, stream) -> None:
     _check(_overlap(a, b, B, k, N, count, stream), "ic_index_overlap")
+
+
+def ic_rope(x, x_token_stride, x_head_stride, pos, freq, mscale, layout, transpose, dtype, T, H, D, rot_off, rot_dim,
+            out, out_token_stride, out_head_stride, stream) -> None:
+    _check(_rope(x, x_token_stride, x_head_stride, pos, freq, mscale, layout, transpose, dtype, T, H, D, rot_off,
+                 rot_dim, out, out_token_stride, out_head_stride, stream), "ic_rope")
+
+
+def ic_latent_append(kv, kv_stride, slots, pos, freq, mscale, layout, T, cache_dtype, cache, num_pages, page_size,
+                     page_stride, workspace, ws_bytes, stream) -> None:
+    _check(_lat_append(kv, kv_stride, slots, pos, freq, mscale, layout, T, cache_dtype, cache, num_pages, page_size,
+                       page_stride, workspace, ws_bytes, stream), "ic_latent_append")
+
+
+def ic_latent_append_workspace_size() -> int:
+    return int(_lat_append_ws())
+
+
+def ic_latent_read(cache, cache_dtype, num_pages, page_size, page_stride, block_table, table_stride, table_width,
+                   cu_len, B, out, R, workspace, ws_bytes, stream) -> None:
+    _check(_lat_read(cache, cache_dtype, num_pages, page_size, page_stride, block_table, table_stride, table_width,
+                     cu_len, B, out, R, workspace, ws_bytes, stream), "ic_latent_read")
+
+
+def ic_latent_read_workspace_size() -> int:
+    return int(_lat_read_ws())
+
+
+def ic_latent_decode(q, cache, cache_dtype, num_pages, page_size, page_stride, block_table, table_stride, table_width,
+                     lens, sink, gate, sm_scale, B, Q, H, out_dtype, out, lse, workspace, ws_bytes, stream) -> None:
+    _check(_lat_decode(q, cache, cache_dtype, num_pages, page_size, page_stride, block_table, table_stride,
+                       table_width, lens, sink, gate, sm_scale, B, Q, H, out_dtype, out, lse, workspace, ws_bytes,
+                       stream), "ic_latent_decode")
+
+
+def ic_latent_decode_workspace_size(B, Q, H, max_len) -> int:
+    return int(_lat_decode_ws(B, Q, H, max_len))
+
+
+def ic_latent_sparse_decode(q, cache, num_pages, page_size, page_stride, slots, k, sink, gate, sm_scale, B, H,
+                            out_dtype, out, lse, workspace, ws_bytes, stream) -> None:
+    _check(_lat_sparse(q, cache, num_pages, page_size, page_stride, slots, k, sink, gate, sm_scale, B, H, out_dtype,
+                       out, lse, workspace, ws_bytes, stream), "ic_latent_sparse_decode")
+
+
+def ic_latent_sparse_workspace_size(B, H, k) -> int:
+    return int(_lat_sparse_ws(B, H, k))
 
 
 IC_CP_MAX_CANDIDATES = 16384

@@ -408,6 +408,118 @@ ic_status_t mla_impl(const void* q, const void* kv, int64_t kv_batch_stride, int
   return IC_OK;
 }
 
+// ------------------------------------------------------------------ paged latent cache
+// A page of rows: page_size a multiple of 16 (a 64-key tile is then whole
+// 16-row boxes of single pages), rows dense within a page, pages page_stride
+// bytes apart.
+bool paged_cache_ok(const void* cache, ic_dtype_t dtype, int64_t num_pages, int page_size, int64_t page_stride) {
+  if (!cache || !aligned16(cache)) return false;
+  if (num_pages < 1 || page_size < 16 || page_size % 16 != 0) return false;
+  if (num_pages > (int64_t(1) << 31) - 1 - 64) return false;
+  const int64_t row = dtype == IC_FP8_E4M3 ? ic::kLatentRowFp8 : ic::kLatentRowBf16;
+  return page_stride >= row * page_size && page_stride % 16 == 0;
+}
+
+// Shares of the tiles: one CTA per SM for the blocks of 64 query rows of each
+// share, but no more shares than two-tile pieces of the longest contexts.
+int latent_groups(int64_t max_tiles, int rblocks) {
+  const int64_t g = std::max(1, num_sms() / rblocks);
+  return static_cast<int>(std::min<int64_t>(g, std::max<int64_t>(1, ceil_div<int64_t>(max_tiles, 2))));
+}
+
+struct LatentLayout {
+  int rblocks, groups;
+  size_t o_off, ml_off, total;
+};
+
+LatentLayout latent_layout(int64_t B, int64_t rows, int64_t max_len) {
+  LatentLayout L{};
+  L.rblocks = static_cast<int>(ceil_div<int64_t>(rows, ic::kLatentTile));
+  L.groups = latent_groups(B * ceil_div<int64_t>(max_len, ic::kLatentTile), L.rblocks);
+  const size_t pieces = size_t(2) * L.groups * L.rblocks * ic::kLatentTile;
+  L.o_off = kStatusBytes;
+  L.ml_off = align256(L.o_off + pieces * 512 * 4);
+  L.total = align256(L.ml_off + pieces * 2 * 4);
+  return L;
+}
+
+ic_status_t latent_impl(const void* q, const void* cache, ic_dtype_t dtype, int64_t num_pages, int page_size,
+                        int64_t page_stride, const int32_t* table, int64_t table_stride, int table_width,
+                        const int64_t* lens, const int32_t* slots, int k, const float* sink, const void* gate,
+                        float sm_scale, int B, int Q, int H, ic_dtype_t out_dtype, void* out, float* lse,
+                        void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  const bool sparse = slots != nullptr, fp8 = dtype == IC_FP8_E4M3;
+  if (!q || !out || !workspace || !aligned16(workspace)) return IC_ERR_INVALID_ARG;
+  if (B < 1 || Q < 1 || H < 1) return IC_ERR_INVALID_ARG;
+  if (!paged_cache_ok(cache, dtype, num_pages, page_size, page_stride)) return IC_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || sm_scale == INFINITY) return IC_ERR_INVALID_ARG;
+  if (out_dtype != IC_BF16 && out_dtype != IC_F32) return IC_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || (gate && !aligned16(gate))) return IC_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(Q) * H;
+  const int64_t max_len = sparse ? k : static_cast<int64_t>(table_width) * page_size;
+  if (max_len >= (int64_t(1) << 31) - 64) return IC_ERR_INVALID_ARG;
+  // one CTA row block (or one joining CTA) each, and q's rows, in 31 bits
+  if (rows * B >= (int64_t(1) << 31) - 64) return IC_ERR_INVALID_ARG;
+  const LatentLayout L = latent_layout(B, rows, max_len);
+  if (ws_bytes < L.total) return IC_ERR_INVALID_ARG;
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return IC_ERR_CUDA;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUtensorMap qmap;
+  {
+    const cuuint64_t dims[2] = {576, static_cast<cuuint64_t>(rows * B)};
+    const cuuint64_t strides[1] = {576 * 2};
+    const cuuint32_t box[2] = {64, 64};
+    if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return IC_ERR_INVALID_ARG;
+  }
+  CUtensorMap kvmap = qmap;  // e4m3 pages are copied without a map
+  if (!fp8) {
+    const cuuint32_t br = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+    const cuuint64_t dims[3] = {576, static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[2] = {ic::kLatentRowBf16, static_cast<cuuint64_t>(page_stride)};
+    const cuuint32_t box[3] = {64, br, 1};
+    if (enc(&kvmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(cache), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return IC_ERR_INVALID_ARG;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ic::LatentArgs a{};
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.page_stride = page_stride;
+  a.page_size = page_size;
+  a.num_pages = static_cast<int>(num_pages);
+  a.table = table;
+  a.table_stride = table_stride;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.slots = slots;
+  a.k = k;
+  a.B = B;
+  a.Q = Q;
+  a.H = H;
+  a.rows = static_cast<int>(rows);
+  a.rblocks = L.rblocks;
+  a.groups = L.groups;
+  a.sink = sink;
+  a.gate = static_cast<const __nv_bfloat16*>(gate);
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.out_f32 = out_dtype == IC_F32 ? 1 : 0;
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  a.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
+  a.status = reinterpret_cast<int*>(ws);
+  a.wait_ns = ic::wait_limit_ns();
+  int launches = 0;
+  if (ic::launch_latent_attention(qmap, kvmap, a, fp8, sparse, stream, &launches) != cudaSuccess) return IC_ERR_CUDA;
+  g_launches = launches;
+  return IC_OK;
+}
+
 // ------------------------------------------------------------------ stack
 struct StackLayout {
   size_t fused_off, mla_off, total;
@@ -766,6 +878,152 @@ ic_status_t ic_cp_combine(const float* part_out, int64_t out_stride, const float
   if (ic::launch_cp_combine(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return IC_ERR_CUDA;
   g_launches = 1;
   return IC_OK;
+}
+
+ic_status_t ic_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int64_t* pos,
+                    const double* freq, float mscale, ic_rope_layout_t layout, int transpose, ic_dtype_t dtype, int64_t T,
+                    int H, int D, int rot_off, int rot_dim, void* out, int64_t out_token_stride,
+                    int64_t out_head_stride, ic_stream_t stream) {
+  g_launches = 0;
+  if (!x || !pos || !freq || !out) return IC_ERR_INVALID_ARG;
+  if (layout != IC_ROPE_INTERLEAVED && layout != IC_ROPE_HALF) return IC_ERR_INVALID_ARG;
+  if (dtype != IC_BF16 && dtype != IC_F32) return IC_ERR_UNSUPPORTED;
+  if (T < 1 || T >= (int64_t(1) << 31) || H < 1 || H > 65535 || D < 2 || D > 65536) return IC_ERR_INVALID_ARG;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_off < 0 || rot_off > D - rot_dim) return IC_ERR_INVALID_ARG;
+  if (rot_dim > 1024) return IC_ERR_UNSUPPORTED;
+  if (!std::isfinite(mscale)) return IC_ERR_INVALID_ARG;
+  const uintptr_t es = dtype == IC_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es) return IC_ERR_INVALID_ARG;
+  // every (token, head) row of the output is its own memory
+  const int64_t ts = out_token_stride, hs = out_head_stride;
+  if (x_token_stride < 0 || x_head_stride < 0 || ts < 0 || hs < 0) return IC_ERR_INVALID_ARG;
+  const bool heads_inner = (H == 1 || hs >= D) && (T == 1 || ts >= (H == 1 ? D : (H - 1) * hs + D));
+  const bool tokens_inner = (T == 1 || ts >= D) && (H == 1 || hs >= (T == 1 ? D : (T - 1) * ts + D));
+  if (!heads_inner && !tokens_inner) return IC_ERR_INVALID_ARG;
+  if (x == out && ((T > 1 && x_token_stride != ts) || (H > 1 && x_head_stride != hs))) return IC_ERR_INVALID_ARG;
+  ic::RopeArgs a{};
+  a.x = x;
+  a.x_ts = T > 1 ? x_token_stride : 0;
+  a.x_hs = H > 1 ? x_head_stride : 0;
+  a.pos = pos;
+  a.freq = freq;
+  a.mscale = mscale;
+  a.half = layout == IC_ROPE_HALF ? 1 : 0;
+  a.transpose = transpose ? 1 : 0;
+  a.T = T;
+  a.H = H;
+  a.D = D;
+  a.rot_off = rot_off;
+  a.rot_dim = rot_dim;
+  a.out = out;
+  a.y_ts = T > 1 ? ts : 0;
+  a.y_hs = H > 1 ? hs : 0;
+  if (ic::launch_rope(a, dtype == IC_F32, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return IC_ERR_CUDA;
+  g_launches = 1;
+  return IC_OK;
+}
+
+size_t ic_latent_append_workspace_size(void) { return kStatusBytes; }
+
+ic_status_t ic_latent_append(const void* kv, int64_t kv_stride, const int64_t* slots, const int64_t* pos,
+                             const double* freq, float mscale, ic_rope_layout_t layout, int64_t T, ic_dtype_t cache_dtype,
+                             void* cache, int64_t num_pages, int page_size, int64_t page_stride, void* workspace,
+                             size_t ws_bytes, ic_stream_t stream) {
+  g_launches = 0;
+  if (!workspace || ws_bytes < kStatusBytes || !aligned16(workspace)) return IC_ERR_INVALID_ARG;
+  if (!kv || !slots || T < 1 || T >= (int64_t(1) << 31)) return IC_ERR_INVALID_ARG;
+  if (cache_dtype != IC_BF16 && cache_dtype != IC_FP8_E4M3) return IC_ERR_UNSUPPORTED;
+  if (!paged_cache_ok(cache, cache_dtype, num_pages, page_size, page_stride)) return IC_ERR_INVALID_ARG;
+  if (!aligned16(kv) || kv_stride < 0 || (T > 1 && kv_stride < 576) || kv_stride % 8 != 0) return IC_ERR_INVALID_ARG;
+  if ((pos != nullptr) != (freq != nullptr)) return IC_ERR_INVALID_ARG;
+  if (pos && ((layout != IC_ROPE_INTERLEAVED && layout != IC_ROPE_HALF) || !std::isfinite(mscale)))
+    return IC_ERR_INVALID_ARG;
+  ic::LatentAppendArgs a{};
+  a.kv = static_cast<const __nv_bfloat16*>(kv);
+  a.kv_stride = T > 1 ? kv_stride : 0;
+  a.slots = slots;
+  a.pos = pos;
+  a.freq = freq;
+  a.mscale = mscale;
+  a.half = layout == IC_ROPE_HALF ? 1 : 0;
+  a.T = T;
+  a.cache = cache;
+  a.page_stride = page_stride;
+  a.page_size = page_size;
+  a.num_slots = num_pages * page_size;
+  a.status = static_cast<int*>(workspace);
+  if (ic::launch_latent_append(a, cache_dtype == IC_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return IC_ERR_CUDA;
+  g_launches = 1;
+  return IC_OK;
+}
+
+size_t ic_latent_read_workspace_size(void) { return kStatusBytes; }
+
+ic_status_t ic_latent_read(const void* cache, ic_dtype_t cache_dtype, int64_t num_pages, int page_size,
+                           int64_t page_stride, const int32_t* block_table, int64_t table_stride, int table_width,
+                           const int64_t* cu_len, int B, void* out, int64_t R, void* workspace, size_t ws_bytes,
+                           ic_stream_t stream) {
+  g_launches = 0;
+  if (!workspace || ws_bytes < kStatusBytes || !aligned16(workspace)) return IC_ERR_INVALID_ARG;
+  if (!block_table || !cu_len || !out || B < 1 || table_width < 1 || R < 1) return IC_ERR_INVALID_ARG;
+  if (cache_dtype != IC_BF16 && cache_dtype != IC_FP8_E4M3) return IC_ERR_UNSUPPORTED;
+  if (!paged_cache_ok(cache, cache_dtype, num_pages, page_size, page_stride)) return IC_ERR_INVALID_ARG;
+  if (!aligned16(out) || table_stride < 0 || (B > 1 && table_stride < table_width)) return IC_ERR_INVALID_ARG;
+  if (R >= (int64_t(1) << 35)) return IC_ERR_INVALID_ARG;
+  ic::LatentReadArgs a{};
+  a.cache = cache;
+  a.page_stride = page_stride;
+  a.page_size = page_size;
+  a.num_pages = static_cast<int>(num_pages);
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.table_width = table_width;
+  a.cu = cu_len;
+  a.B = B;
+  a.R = R;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.status = static_cast<int*>(workspace);
+  if (ic::launch_latent_read(a, cache_dtype == IC_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return IC_ERR_CUDA;
+  g_launches = 1;
+  return IC_OK;
+}
+
+size_t ic_latent_decode_workspace_size(int B, int Q, int H, int64_t max_len) {
+  if (B < 1 || Q < 1 || H < 1 || max_len < 1) return kStatusBytes;
+  return latent_layout(B, static_cast<int64_t>(Q) * H, max_len).total;
+}
+
+ic_status_t ic_latent_decode(const void* q, const void* cache, ic_dtype_t cache_dtype, int64_t num_pages,
+                             int page_size, int64_t page_stride, const int32_t* block_table, int64_t table_stride,
+                             int table_width, const int64_t* lens, const float* sink, const void* gate, float sm_scale,
+                             int B, int Q, int H, ic_dtype_t out_dtype, void* out, float* lse, void* workspace,
+                             size_t ws_bytes, ic_stream_t stream) {
+  g_launches = 0;
+  if (!block_table || !lens || table_width < 1 || table_stride < 0 || (B > 1 && table_stride < table_width))
+    return IC_ERR_INVALID_ARG;
+  if (cache_dtype != IC_BF16 && cache_dtype != IC_FP8_E4M3) return IC_ERR_UNSUPPORTED;
+  return latent_impl(q, cache, cache_dtype, num_pages, page_size, page_stride, block_table, table_stride, table_width,
+                     lens, nullptr, 0, sink, gate, sm_scale, B, Q, H, out_dtype, out, lse, workspace, ws_bytes,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t ic_latent_sparse_workspace_size(int B, int H, int k) {
+  if (B < 1 || H < 1 || k < 1) return kStatusBytes;
+  return latent_layout(B, H, k).total;
+}
+
+ic_status_t ic_latent_sparse_decode(const void* q, const void* cache, int64_t num_pages, int page_size,
+                                    int64_t page_stride, const int32_t* slots, int k, const float* sink,
+                                    const void* gate, float sm_scale, int B, int H, ic_dtype_t out_dtype, void* out,
+                                    float* lse, void* workspace, size_t ws_bytes, ic_stream_t stream) {
+  g_launches = 0;
+  if (!slots || k < 1) return IC_ERR_INVALID_ARG;
+  if (num_pages >= 1 && page_size >= 1 && num_pages > ((int64_t(1) << 31) - 1) / page_size) return IC_ERR_INVALID_ARG;
+  return latent_impl(q, cache, IC_FP8_E4M3, num_pages, page_size, page_stride, nullptr, 0, 0, nullptr, slots, k, sink,
+                     gate, sm_scale, B, 1, H, out_dtype, out, lse, workspace, ws_bytes,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 ic_status_t ic_last_device_status(void* workspace, ic_stream_t stream) {

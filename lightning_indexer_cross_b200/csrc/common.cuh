@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -253,6 +254,27 @@ IC_DEV void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The weight-stationary form: with M = 64 the accumulator fills all 128 lanes
+// of N / 2 columns (lane l < 64: row l, columns [0, N / 2); lane 64 + l: row l,
+// columns [N / 2, N)), so a 64 x 512 output takes 256 columns, not 512.
+IC_DEV void mma_ws_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One lane of a fully active warp; the compiler then issues the lane's MMAs
+// from the uniform datapath (measured on B200: 16 to 32 cycles an issue,
+// against 96 under a lane == 0 test).
+IC_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // Arrive (once) on `bar` when every tcgen05.mma issued so far by this thread
 // has completed.
 IC_DEV void mma_commit(uint64_t* bar) {
@@ -286,6 +308,21 @@ IC_DEV void tmem_ld_wait(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+
+// 32 columns of registers to TMEM; tmem_st_wait before another thread or an
+// MMA uses them.
+IC_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+IC_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 2^x with the hardware approximation (relative error ~2^-22; -inf -> +0).
 IC_DEV float ex2_approx(float x) {
@@ -384,6 +421,37 @@ IC_DEV float bf16_lane(uint32_t w, int e) { return __uint_as_float(e ? (w & 0xff
 IC_DEV uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+// Sixteen e4m3 codes times a scale as bf16 (eight packed pairs, lowest byte
+// first). Exact where the scale is a power of two; otherwise each product is
+// rounded to bf16.
+IC_DEV void e4m3x16_to_bf16x16(const uint4& c, float scale, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16x4(w[i], lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    o[2 * i] = pack_bf16x2(a.x * scale, a.y * scale);
+    o[2 * i + 1] = pack_bf16x2(b.x * scale, b.y * scale);
+  }
+}
+
+// ---------------------------------------------------------------- rotary angle
+// mscale cos and mscale sin (negated if `transpose`) of position * freq. The
+// product (x plus its rounding error e) is reduced to [-pi, pi] in 64 bits
+// with 2 pi in two parts; the sine and cosine of the reduced angle are 32-bit.
+IC_DEV float2 rope_cos_sin(int64_t position, double freq, float mscale, bool transpose) {
+  const double p = static_cast<double>(position);
+  const double x = p * freq;
+  const double e = fma(p, freq, -x);
+  const double k = rint(x * 0.15915494309189533577);  // 1 / (2 pi)
+  double r = fma(-k, 6.28318530717958623200, x);      // 2 pi, high part
+  r = fma(-k, 2.44929359829470641435e-16, r) + e;     // 2 pi, low part
+  float s, c;
+  sincosf(static_cast<float>(r), &s, &c);
+  return make_float2(mscale * c, transpose ? -mscale * s : mscale * s);
 }
 
 }  // namespace ic

@@ -210,6 +210,93 @@ struct AppendArgs {
 };
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- rotary positions
+struct RopeArgs {
+  const void* x;       // [T, H, D], innermost dense
+  int64_t x_ts, x_hs;  // elements between tokens and heads
+  const int64_t* pos;  // [T]
+  const double* freq;  // [rot_dim / 2]
+  float mscale;
+  int half;            // pairs (i, i + rot_dim / 2) instead of (2i, 2i + 1)
+  int transpose;       // the transposed map
+  int64_t T;
+  int H, D, rot_off, rot_dim;
+  void* out;
+  int64_t y_ts, y_hs;
+};
+cudaError_t launch_rope(const RopeArgs& a, bool f32, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged latent cache
+// Bytes of a row of the paged latent cache.
+constexpr int kLatentRowBf16 = 1152;
+constexpr int kLatentRowFp8 = 656;
+
+struct LatentAppendArgs {
+  const __nv_bfloat16* kv;  // [T, 576], kv_stride elements between rows
+  int64_t kv_stride;
+  const int64_t* slots;     // [T] page * page_size + row, or -1
+  const int64_t* pos;       // [T] or null: the rotary dims are stored as given
+  const double* freq;       // [32]
+  float mscale;
+  int half;
+  int64_t T;
+  void* cache;
+  int64_t page_stride;      // bytes
+  int page_size;
+  int64_t num_slots;        // num_pages * page_size
+  int* status;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, bool fp8, cudaStream_t stream);
+
+struct LatentReadArgs {
+  const void* cache;
+  int64_t page_stride;  // bytes
+  int page_size, num_pages;
+  const int32_t* table;  // [B, table_width]
+  int64_t table_stride;
+  int table_width;
+  const int64_t* cu;     // [B + 1] first output row of each sequence
+  int B;
+  int64_t R;             // rows of out
+  __nv_bfloat16* out;    // [R, 576]
+  int* status;
+};
+cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t stream);
+
+// ---------------------------------------------------------------- attention over the paged latent cache
+constexpr int kLatentTile = 64;  // keys of a tile, and query rows of a block
+
+struct LatentArgs {
+  const uint8_t* cache;
+  int64_t page_stride;   // bytes
+  int page_size, num_pages;
+  const int32_t* table;  // dense: [B, table_width] page numbers
+  int64_t table_stride;
+  int table_width;
+  const int64_t* lens;   // dense: [B]
+  const int32_t* slots;  // sparse: [B, k]
+  int k;
+  int B, Q, H;
+  int rows;              // Q * H query rows of a sequence
+  int rblocks;           // ceil(rows / 64)
+  int groups;            // shares of the tiles; groups * rblocks CTAs
+  const float* sink;     // [H] or null
+  const __nv_bfloat16* gate;  // [B, Q, H, 512] or null
+  float sm_scale;
+  void* out;             // [B, Q, H, 512]
+  int out_f32;
+  float* lse;            // [B, Q, H] or null
+  float* part_o;         // [2 groups][rblocks][64][512]
+  float* part_ml;        // [2 groups][rblocks][64][2]
+  int* status;
+  uint64_t wait_ns;
+};
+// qmap: 2-D map over q as [B * rows, 576] bf16, box 64 x 64, 128-byte swizzle.
+// kvmap (bf16 pages): 3-D map (576, page_size, num_pages), box 64 x box_rows x 1,
+// 128-byte swizzle; e4m3 pages are copied without a map (any valid map).
+cudaError_t launch_latent_attention(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, bool fp8,
+                                    bool sparse, cudaStream_t stream, int* launches);
+
 // ---------------------------------------------------------------- output gate
 struct GateArgs {
   const __nv_bfloat16* gate;  // [B, H, 128] or null (identity)

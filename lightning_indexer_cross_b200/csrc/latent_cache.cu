@@ -1,0 +1,216 @@
+// The paged latent cache on sm_100a: rows written into pages, and read back.
+//
+// A page holds page_size rows. A bf16 row is the 576 values themselves
+// (512 latent, 64 rotary). An e4m3 row is 656 bytes:
+//   [0, 512)   e4m3 codes of the latent dims
+//   [512, 528) four fp32 scales, one for each 128 dims
+//   [528, 656) the 64 rotary values in bf16
+// value = code * scale with scale = 2^e, the least power of two that is at
+// least max|y| / 448 over the 128 dims (1 where all are zero, e >= -100). With
+// a power of two the division by the scale is exact, and so is the decoded
+// value in bf16 (4 significant bits): the only rounding is that of y / scale
+// to e4m3 (nearest even, at most half a step, 2^-4 of the value), and a reader
+// may form the products of a row in bf16 without a second one.
+//
+// Both kernels move each byte once, one warp a token with 16-byte words, and
+// are bound by HBM for long runs and by launch latency at decode sizes.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace ic {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (t >= a.T) return;
+  const int64_t slot = a.slots[t];
+  // this lane's 16 latent values and its rotary pair, requested before the
+  // slot is known
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(a.kv) + t * a.kv_stride * 2;
+  const uint4 w0 = *reinterpret_cast<const uint4*>(src + lane * 32);
+  const uint4 w1 = *reinterpret_cast<const uint4*>(src + lane * 32 + 16);
+  uint32_t rot = *reinterpret_cast<const uint32_t*>(
+      src + 1024 + 4 * lane);
+  if (slot < 0 || slot >= a.num_slots) {
+    if (slot != -1 && lane == 0) record_status(a.status, IC_ERR_BAD_INDEX);
+    return;
+  }
+  const int64_t page = slot / a.page_size;
+  const int off = static_cast<int>(slot - page * a.page_size);
+  uint8_t* dst = static_cast<uint8_t*>(a.cache) + page * a.page_stride + static_cast<int64_t>(off) * (FP8 ? 656 : 1152);
+  uint8_t* rdst = dst + (FP8 ? 528 : 1024);
+  if (a.pos) {
+    const int64_t p = a.pos[t];
+    if (a.half) {
+      // dims i and i + 32: lane i (< 16) holds dims 2i, 2i + 1; their partners
+      // are in lane i + 16
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, rot, 16);
+      const int i0 = (lane & 15) * 2;
+      float y[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 r = rope_cos_sin(p, a.freq[i0 + e], a.mscale, false);
+        const float mine = bf16_lane(rot, e), theirs = bf16_lane(other, e);
+        y[e] = lane < 16 ? mine * r.x - theirs * r.y : theirs * r.y + mine * r.x;
+      }
+      rot = pack_bf16x2(y[0], y[1]);
+    } else {
+      const float2 r = rope_cos_sin(p, a.freq[lane], a.mscale, false);
+      const float u = bf16_lane(rot, 0), v = bf16_lane(rot, 1);
+      rot = pack_bf16x2(u * r.x - v * r.y, u * r.y + v * r.x);
+    }
+  }
+  *reinterpret_cast<uint32_t*>(rdst + 4 * lane) = rot;
+  if constexpr (!FP8) {
+    *reinterpret_cast<uint4*>(dst + lane * 32) = w0;
+    *reinterpret_cast<uint4*>(dst + lane * 32 + 16) = w1;
+  } else {
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    // largest finite |y| of the 128 dims (8 lanes)
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = fabsf(bf16_lane(w[i >> 1], i & 1));
+      if (x < INFINITY) amax = fmaxf(amax, x);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // amax = m 2^E with m in [1, 2); 448 = 1.75 2^8: the least e with
+    // 2^e >= amax / 448 is E - 8, or E - 7 where m > 1.75
+    int e = 0;
+    if (amax > 0.f) {
+      const uint32_t bits = __float_as_uint(amax);  // a bf16 subnormal (E = -127 here) ends at e = -100 all the same
+      e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+      e = e < -100 ? -100 : e;
+    }
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, -e in [-119, 100]
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p0 = make_float2(bf16_lane(w[2 * i], 0) * inv, bf16_lane(w[2 * i], 1) * inv);
+      const float2 p1 = make_float2(bf16_lane(w[2 * i + 1], 0) * inv, bf16_lane(w[2 * i + 1], 1) * inv);
+      c[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p0, __NV_SATFINITE, __NV_E4M3)) |
+             (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p1, __NV_SATFINITE, __NV_E4M3)) << 16);
+    }
+    *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    if ((lane & 7) == 0)
+      *reinterpret_cast<float*>(dst + 512 + (lane >> 3) * 4) = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  }
+}
+
+// Output row r belongs to sequence b with cu[b] <= r < cu[b + 1]. A CTA takes
+// kRows consecutive rows, its warps kRows / kWarps each.
+constexpr int kRowsPerWarp = 4;
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsPerWarp;
+  int64_t end = a.cu[a.B];
+  if (end > a.R) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_status(a.status, IC_ERR_BAD_INDEX);
+    end = a.R;
+  }
+  if (r0 >= end) return;
+  // the last b with cu[b] <= r0
+  int lo = 0, hi = a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cu[mid] <= r0) lo = mid; else hi = mid - 1;
+  }
+  int b = lo;
+  const uint8_t* src[kRowsPerWarp];
+#pragma unroll
+  for (int j = 0; j < kRowsPerWarp; ++j) {
+    const int64_t r = r0 + j;
+    src[j] = nullptr;
+    if (r < end) {
+      while (b + 1 < a.B && a.cu[b + 1] <= r) ++b;
+      const int64_t p = r - a.cu[b];
+      const int64_t pi = p / a.page_size;
+      int page = -1;
+      if (p >= 0 && pi < a.table_width) page = a.table[static_cast<int64_t>(b) * a.table_stride + pi];
+      if (page >= 0 && page < a.num_pages)
+        src[j] = static_cast<const uint8_t*>(a.cache) + page * a.page_stride +
+                 (p - pi * a.page_size) * (FP8 ? 656 : 1152);
+      else if (lane == 0)
+        record_status(a.status, IC_ERR_BAD_INDEX);
+    }
+  }
+  if constexpr (!FP8) {
+    // 72 words of 16 bytes a row
+    uint4 w[kRowsPerWarp][3];
+#pragma unroll
+    for (int j = 0; j < kRowsPerWarp; ++j)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        w[j][k] = make_uint4(0, 0, 0, 0);
+        if (src[j] && lane + 32 * k < 72) w[j][k] = *reinterpret_cast<const uint4*>(src[j] + (lane + 32 * k) * 16);
+      }
+#pragma unroll
+    for (int j = 0; j < kRowsPerWarp; ++j)
+      if (r0 + j < end) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (r0 + j) * 576);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (lane + 32 * k < 72) dst[lane + 32 * k] = w[j][k];
+      }
+  } else {
+    uint4 c[kRowsPerWarp];
+    uint32_t rot[kRowsPerWarp];
+    float s[kRowsPerWarp];
+#pragma unroll
+    for (int j = 0; j < kRowsPerWarp; ++j) {
+      c[j] = make_uint4(0, 0, 0, 0);
+      rot[j] = 0;
+      s[j] = 0.f;
+      if (src[j]) {
+        c[j] = *reinterpret_cast<const uint4*>(src[j] + lane * 16);
+        s[j] = *reinterpret_cast<const float*>(src[j] + 512 + (lane >> 3) * 4);
+        rot[j] = *reinterpret_cast<const uint32_t*>(src[j] + 528 + lane * 4);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsPerWarp; ++j)
+      if (r0 + j < end) {
+        uint32_t o[8];
+        e4m3x16_to_bf16x16(c[j], s[j], o);
+        uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + (r0 + j) * 576);
+        *reinterpret_cast<uint4*>(dst + lane * 32) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + lane * 32 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint32_t*>(dst + 1024 + lane * 4) = rot[j];
+      }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentAppendArgs& a, bool fp8, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((a.T + kWarps - 1) / kWarps);
+  if (fp8)
+    latent_append_kernel<true><<<grid, kThreads, 0, stream>>>(a);
+  else
+    latent_append_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t stream) {
+  constexpr int kRows = kWarps * kRowsPerWarp;
+  const unsigned grid = static_cast<unsigned>((a.R + kRows - 1) / kRows);
+  if (fp8)
+    latent_read_kernel<true><<<grid, kThreads, 0, stream>>>(a);
+  else
+    latent_read_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace ic

@@ -7,6 +7,7 @@ allocate outputs and workspaces with torch, and pass raw pointers through
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import List, Optional, Sequence
@@ -323,6 +324,283 @@ def reuse_overlap(layers: Sequence, schedule: str, topk: int, n_valid: Optional[
         elif last is not None:
             own[l] = index_overlap(last, idx, N, stream=stream)
     return own
+
+
+LATENT_ROW_BYTES = 656  # an e4m3 row of the paged latent cache
+_ROPE_LAYOUT = {"interleaved": _abi.IC_ROPE_INTERLEAVED, "half": _abi.IC_ROPE_HALF}
+
+
+def _same_device(*ts) -> torch.device:
+    """The one CUDA device of the given tensors (None entries aside)."""
+    _need_cuda(*ts)
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+def _on(dev: torch.device, stream):
+    """Context that makes `dev` and the launch's stream current: outputs and workspaces made inside are that
+    stream's, so neither their zeroing nor their reuse can overtake the launch."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> torch.Tensor:
+    """The given byte workspace, or a new one of which only the status word is cleared."""
+    if workspace is None:
+        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+        workspace[:256].zero_()
+        return workspace
+    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous(),
+          "the workspace is a uint8 vector")
+    return workspace
+
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[dict] = None, device="cuda"):
+    """(freq, mscale) for ``rope`` and ``latent_append``: freq [rot_dim / 2] float64, base^(-2i / rot_dim), scaled
+    for contexts longer than the trained one:
+
+    * ``{"type": "linear", "factor": s}``: every frequency divided by s;
+    * ``{"type": "yarn", "factor": s, "original_length": L}`` (Peng et al., YaRN): frequencies that turn more than
+      ``beta_fast`` (32) times over L stay, those that turn less than ``beta_slow`` (1) times are divided by s, a
+      linear ramp over the index between; mscale = 0.1 ``mscale`` ln s + 1 (``mscale`` 1 by default)."""
+    _need(rot_dim >= 2 and rot_dim % 2 == 0 and base > 0 and math.isfinite(base), "rot_dim even, base > 0")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    freq = float(base) ** (-2.0 * i / rot_dim)
+    mscale = 1.0
+    if scaling is not None:
+        s = float(scaling["factor"])
+        _need(s > 0 and math.isfinite(s), "scaling factor > 0")
+        if scaling["type"] == "linear":
+            freq = freq / s
+        elif scaling["type"] == "yarn":
+            L = float(scaling["original_length"])
+
+            def index_of(turns):  # the index whose frequency turns that many times over L
+                return rot_dim * math.log(L / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+            lo = max(math.floor(index_of(float(scaling.get("beta_fast", 32)))), 0)
+            hi = min(math.ceil(index_of(float(scaling.get("beta_slow", 1)))), rot_dim - 1)
+            ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            freq = freq * (1 - ramp) + freq / s * ramp
+            if s > 1:
+                mscale = 0.1 * float(scaling.get("mscale", 1.0)) * math.log(s) + 1.0
+        else:
+            raise ValueError(f"unknown scaling type {scaling['type']!r}")
+    return freq.to(device), mscale
+
+
+def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, rot_off: int = 0, layout: str = "interleaved",
+         mscale: float = 1.0, transpose: bool = False, out: Optional[torch.Tensor] = None,
+         stream=None) -> torch.Tensor:
+    """Rotary positions: x [T, H, D] (bf16 or fp32, innermost dense) with dims [rot_off, rot_off + 2 len(freq)) of
+    every head rotated to pos [T] (int64); the other dims are copied. layout: "interleaved" pairs (2i, 2i + 1) or
+    "half" pairs (i, i + len(freq)). transpose=True applies the transposed map (the gradient's). out may be x."""
+    dev = _same_device(x, pos, freq, out)
+    _need(x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32), "x is [T, H, D], bf16 or fp32")
+    T, H, D = x.shape
+    rot = 2 * freq.numel()
+    _need(x.stride(2) == 1, "x is dense along D")
+    _need(pos.shape == (T,) and pos.dtype == torch.int64, "pos is int64 [T]")
+    _need(freq.dim() == 1 and freq.dtype == torch.float64, "freq is float64 [rot_dim / 2]")
+    _need(layout in _ROPE_LAYOUT, "layout is interleaved or half")
+    _need(0 <= rot_off and rot_off + rot <= D, "the rotated dims lie in the head")
+    _need_dense(pos, freq)
+    _need(out is None or (out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1),
+          "out is like x, dense along D")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        if T > 0 and H > 0:
+            _abi.ic_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(pos), _ptr(freq), float(mscale), _ROPE_LAYOUT[layout],
+                         int(bool(transpose)), _abi.IC_F32 if x.dtype == torch.float32 else _abi.IC_BF16, T, H, D,
+                         int(rot_off), rot, _ptr(out), out.stride(0), out.stride(1), _stream_ptr())
+    return out
+
+
+def new_latent_cache(num_pages: int, page_size: int, fp8: bool = False, device="cuda") -> torch.Tensor:
+    """A zeroed paged latent cache: [num_pages, page_size, 576] bf16, or [num_pages, page_size, 656] uint8 whose rows
+    hold 512 e4m3 codes, four fp32 scales and 64 bf16 rotary values."""
+    if fp8:
+        return torch.zeros((num_pages, page_size, LATENT_ROW_BYTES), dtype=torch.uint8, device=device)
+    return torch.zeros((num_pages, page_size, D_QK), dtype=torch.bfloat16, device=device)
+
+
+def _latent_cache(cache: torch.Tensor):
+    """(dtype code, num_pages, page_size, page stride in bytes) of a paged latent cache."""
+    _need(cache.dim() == 3, "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8")
+    P, ps, row = cache.shape
+    fp8 = cache.dtype == torch.uint8
+    _need((fp8 and row == LATENT_ROW_BYTES) or (cache.dtype == torch.bfloat16 and row == D_QK),
+          "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8")
+    _need_dense_rows(cache)
+    stride = cache.stride(0) if P > 1 else ps * row
+    return _abi.IC_FP8_E4M3 if fp8 else _abi.IC_BF16, P, ps, stride * cache.element_size()
+
+
+def latent_append(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, pos: Optional[torch.Tensor] = None,
+                  freq: Optional[torch.Tensor] = None, layout: str = "interleaved", mscale: float = 1.0,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Write T latent rows kv [T, 576] bf16 into slots[t] (int64, -1 skips; slot = page * page_size + row) of the
+    paged cache, quantised if it holds e4m3 rows; with pos [T] and freq [32] the 64 rotary dims are rotated as by
+    ``rope``. Returns the workspace (its status word records slots outside the cache)."""
+    dev = _same_device(kv, slots, cache, pos, freq, workspace)
+    code, P, ps, stride = _latent_cache(cache)
+    _need(kv.dim() == 2 and kv.shape[1] == D_QK and kv.dtype == torch.bfloat16, "kv is bf16 [T, 576]")
+    T = kv.shape[0]
+    _need(kv.stride(1) == 1, "kv is dense along a row")
+    _need(slots.shape == (T,) and slots.dtype == torch.int64, "slots is int64 [T]")
+    _need((pos is None) == (freq is None), "pos and freq come together")
+    if pos is not None:
+        _need(pos.shape == (T,) and pos.dtype == torch.int64, "pos is int64 [T]")
+        _need(freq.shape == ((D_QK - D_V) // 2,) and freq.dtype == torch.float64, "freq is float64 [32]")
+    _need(layout in _ROPE_LAYOUT, "layout is interleaved or half")
+    _need_dense(slots, pos, freq)
+    with _on(dev, stream):
+        workspace = _workspace(workspace, _abi.ic_latent_append_workspace_size(), dev)
+        if T > 0:
+            _abi.ic_latent_append(_ptr(kv), kv.stride(0), _ptr(slots), _ptr(pos), _ptr(freq), float(mscale),
+                                  _ROPE_LAYOUT[layout], T, code, _ptr(cache), P, ps, stride, _ptr(workspace),
+                                  workspace.numel(), _stream_ptr())
+    return workspace
+
+
+def latent_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Tensor, out: torch.Tensor,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Copy sequences out of the paged cache: rows cu_len[b] .. cu_len[b + 1] of out [R, 576] bf16 become the first
+    rows of sequence b, found through block_table [B, width] int32; cu_len int64 [B + 1]. Rows behind cu_len[B] are
+    left as they are."""
+    dev = _same_device(cache, block_table, cu_len, out, workspace)
+    code, P, ps, stride = _latent_cache(cache)
+    table_stride = _block_table(block_table)
+    B = block_table.shape[0]
+    _need(cu_len.shape == (B + 1,) and cu_len.dtype == torch.int64, "cu_len is int64 [B + 1]")
+    _need(out.dim() == 2 and out.shape[1] == D_QK and out.dtype == torch.bfloat16, "out is bf16 [R, 576]")
+    _need_dense(cu_len, out)
+    with _on(dev, stream):
+        workspace = _workspace(workspace, _abi.ic_latent_read_workspace_size(), dev)
+        if out.shape[0] > 0:
+            _abi.ic_latent_read(_ptr(cache), code, P, ps, stride, _ptr(block_table), table_stride,
+                                block_table.shape[1], _ptr(cu_len), B, _ptr(out), out.shape[0], _ptr(workspace),
+                                workspace.numel(), _stream_ptr())
+    return out
+
+
+def _block_table(table: torch.Tensor) -> int:
+    _need(table.dim() == 2 and table.dtype == torch.int32 and table.stride(1) == 1 and
+          (table.shape[0] == 1 or table.stride(0) >= table.shape[1]),
+          "block_table is int32 [B, width], dense along a row")
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def _attention_args(q, sink, gate, out, out_dtype, lse):
+    H = q.shape[-2]
+    shape = tuple(q.shape[:-1])
+    _need(q.shape[-1] == D_QK and q.dtype == torch.bfloat16, "q is bf16 [..., H, 576]")
+    _need(sink is None or (sink.shape == (H,) and sink.dtype == torch.float32), "sink is fp32 [H]")
+    _need(gate is None or (gate.shape == shape + (D_V,) and gate.dtype == torch.bfloat16), "gate is bf16 [..., H, 512]")
+    _need(out is None or out.shape == shape + (D_V,), "out is [..., H, 512]")
+    _need((out_dtype if out is None else out.dtype) in (torch.bfloat16, torch.float32), "out is bf16 or fp32")
+    _need(lse is None or (lse.shape == shape and lse.dtype == torch.float32), "lse is fp32 [..., H]")
+    _need_dense(q, sink, gate, out, lse)
+
+
+def _attention_outputs(q, out, out_dtype, lse, want_lse):
+    if out is None:
+        out = torch.empty(q.shape[:-1] + (D_V,), dtype=out_dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    return out, lse
+
+
+def latent_decode_workspace_size(B: int, Q: int, H: int, max_len: int) -> int:
+    """Workspace bytes of ``latent_decode`` (on the current device) for a block table of max_len rows a sequence."""
+    return _abi.ic_latent_decode_workspace_size(B, Q, H, max_len)
+
+
+def latent_sparse_workspace_size(B: int, H: int, k: int) -> int:
+    """Workspace bytes of ``latent_sparse_decode`` (on the current device)."""
+    return _abi.ic_latent_sparse_workspace_size(B, H, k)
+
+
+def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                  sink: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  sm_scale: Optional[float] = None, out_dtype: torch.dtype = torch.bfloat16,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """Dense latent attention over the paged cache: q [B, H, 576] (one new token a sequence) or [B, Q, H, 576] (Q new
+    tokens, token j seeing lens[b] - (Q - 1 - j) rows), block_table [B, width] int32, lens [B] int64 (0: an idle
+    slot). Returns (out [..., H, 512], lse [..., H])."""
+    dev = _same_device(q, cache, block_table, lens, sink, gate, out, lse, workspace)
+    code, P, ps, stride = _latent_cache(cache)
+    table_stride = _block_table(block_table)
+    _need(q.dim() in (3, 4), "q is [B, H, 576] or [B, Q, H, 576]")
+    B, H, Q = q.shape[0], q.shape[-2], (q.shape[1] if q.dim() == 4 else 1)
+    width = block_table.shape[1]
+    _need(block_table.shape[0] == B and lens.shape == (B,) and lens.dtype == torch.int64,
+          "block_table is [B, width], lens int64 [B]")
+    _need_dense(lens)
+    _attention_args(q, sink, gate, out, out_dtype, lse)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D_QK)
+    with _on(dev, stream):
+        out, lse = _attention_outputs(q, out, out_dtype, lse, want_lse)
+        if q.numel() > 0:
+            workspace = _workspace(workspace, 0 if workspace is not None else
+                                   _abi.ic_latent_decode_workspace_size(B, Q, H, width * ps), dev)
+            _abi.ic_latent_decode(_ptr(q), _ptr(cache), code, P, ps, stride, _ptr(block_table), table_stride, width,
+                                  _ptr(lens), _ptr(sink), _ptr(gate), float(sm_scale), B, Q, H,
+                                  _abi.IC_F32 if out.dtype == torch.float32 else _abi.IC_BF16, _ptr(out), _ptr(lse),
+                                  _ptr(workspace), workspace.numel(), _stream_ptr())
+    return out, lse
+
+
+def latent_sparse_decode(q: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
+                         sink: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                         sm_scale: Optional[float] = None, out_dtype: torch.dtype = torch.bfloat16,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         want_lse: bool = True, workspace: Optional[torch.Tensor] = None, stream=None):
+    """``sparse_mla_decode`` over an e4m3 paged cache: q [B, H, 576] attends to slots [B, k] (int32, -1 padding) of
+    the cache. Returns (out [B, H, 512], lse [B, H]). (Dense bf16 pages: ``sparse_mla_decode`` with
+    cache.view(1, -1, 576) and the slots as idx.)"""
+    dev = _same_device(q, cache, slots, sink, gate, out, lse, workspace)
+    code, P, ps, stride = _latent_cache(cache)
+    _need(code == _abi.IC_FP8_E4M3, "the cache holds e4m3 rows")
+    _need(q.dim() == 3, "q is [B, H, 576]")
+    B, H, _ = q.shape
+    _need(slots.dim() == 2 and slots.shape[0] == B and slots.dtype == torch.int32, "slots is int32 [B, k]")
+    _need_dense(slots)
+    _attention_args(q, sink, gate, out, out_dtype, lse)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D_QK)
+    k = slots.shape[1]
+    with _on(dev, stream):
+        out, lse = _attention_outputs(q, out, out_dtype, lse, want_lse)
+        if q.numel() > 0:
+            workspace = _workspace(workspace, 0 if workspace is not None else
+                                   _abi.ic_latent_sparse_workspace_size(B, H, k), dev)
+            _abi.ic_latent_sparse_decode(_ptr(q), _ptr(cache), P, ps, stride, _ptr(slots), k, _ptr(sink), _ptr(gate),
+                                         float(sm_scale), B, H,
+                                         _abi.IC_F32 if out.dtype == torch.float32 else _abi.IC_BF16, _ptr(out),
+                                         _ptr(lse), _ptr(workspace), workspace.numel(), _stream_ptr())
+    return out, lse
+
+
+def slots_of(idx: torch.Tensor, block_table: torch.Tensor, page_size: int) -> torch.Tensor:
+    """Positions idx [B, k] (int32, -1 padding; a top-k's output) as slots of a paged cache."""
+    _need(idx.dim() == 2 and block_table.dim() == 2 and idx.shape[0] == block_table.shape[0], "idx [B, k], block_table [B, width]")
+    p = idx.clamp(min=0)
+    page = torch.gather(block_table, 1, (p // page_size).long())
+    return torch.where(idx >= 0, page * page_size + p % page_size, idx).to(torch.int32)
 
 
 class LayerStack:
