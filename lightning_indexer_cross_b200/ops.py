@@ -328,28 +328,43 @@ def reuse_overlap(layers: Sequence, schedule: str, topk: int, n_valid: Optional[
 
 LATENT_ROW_BYTES = 656  # an e4m3 row of the paged latent cache
 _ROPE_LAYOUT = {"interleaved": _abi.IC_ROPE_INTERLEAVED, "half": _abi.IC_ROPE_HALF}
+_ROPE_DTYPE = _OUT_DTYPE = {torch.bfloat16: _abi.IC_BF16, torch.float32: _abi.IC_F32}
+_SM_SCALE = 1.0 / math.sqrt(D_QK)
 
 
-def _same_device(*ts) -> torch.device:
-    """The one CUDA device of the given tensors (None entries aside)."""
-    _need_cuda(*ts)
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+def _elsewhere(x: torch.Tensor, stream) -> bool:
+    """Whether x is on another device than the current one, or a stream is named: the call is then made again inside
+    ``_on``. (The plain case costs no context manager: a decode step's calls take a few microseconds each.)"""
+    _need_cuda(x)
+    return stream is not None or x.get_device() != torch.cuda.current_device()
 
 
-def _on(dev: torch.device, stream):
-    """Context that makes `dev` and the launch's stream current: outputs and workspaces made inside are that
+def _on(x: torch.Tensor, stream):
+    """Context that makes x's device and the launch's stream current: outputs and workspaces made inside are that
     stream's, so neither their zeroing nor their reuse can overtake the launch."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream is None:
+        return torch.cuda.device(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
+    return torch.cuda.stream(stream)
 
 
-def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> torch.Tensor:
+def _same_device(dev: int, *ts) -> None:
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _current_stream(dev: int) -> int:
+    """Handle of dev's current stream, without the object around it (3 us of a call)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> torch.Tensor:
     """The given byte workspace, or a new one of which only the status word is cleared."""
     if workspace is None:
         workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
@@ -405,25 +420,31 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, rot_off: int = 
     """Rotary positions: x [T, H, D] (bf16 or fp32, innermost dense) with dims [rot_off, rot_off + 2 len(freq)) of
     every head rotated to pos [T] (int64); the other dims are copied. layout: "interleaved" pairs (2i, 2i + 1) or
     "half" pairs (i, i + len(freq)). transpose=True applies the transposed map (the gradient's). out may be x."""
-    dev = _same_device(x, pos, freq, out)
-    _need(x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32), "x is [T, H, D], bf16 or fp32")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return rope(x, pos, freq, rot_off, layout, mscale, transpose, out)
+    dev = x.get_device()
+    _same_device(dev, pos, freq, out)
+    _need(x.dim() == 3 and x.dtype in _ROPE_DTYPE, "x is [T, H, D], bf16 or fp32")
     T, H, D = x.shape
+    xt, xh, xd = x.stride()
     rot = 2 * freq.numel()
-    _need(x.stride(2) == 1, "x is dense along D")
+    _need(xd == 1 or D == 1, "x is dense along D")
     _need(pos.shape == (T,) and pos.dtype == torch.int64, "pos is int64 [T]")
     _need(freq.dim() == 1 and freq.dtype == torch.float64, "freq is float64 [rot_dim / 2]")
     _need(layout in _ROPE_LAYOUT, "layout is interleaved or half")
     _need(0 <= rot_off and rot_off + rot <= D, "the rotated dims lie in the head")
     _need_dense(pos, freq)
-    _need(out is None or (out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1),
-          "out is like x, dense along D")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-        if T > 0 and H > 0:
-            _abi.ic_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(pos), _ptr(freq), float(mscale), _ROPE_LAYOUT[layout],
-                         int(bool(transpose)), _abi.IC_F32 if x.dtype == torch.float32 else _abi.IC_BF16, T, H, D,
-                         int(rot_off), rot, _ptr(out), out.stride(0), out.stride(1), _stream_ptr())
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        ot, oh = H * D, D
+    else:
+        _need(out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1, "out is like x, dense along D")
+        ot, oh = out.stride(0), out.stride(1)
+    if T > 0 and H > 0:
+        _abi.ic_rope(x.data_ptr(), xt, xh, pos.data_ptr(), freq.data_ptr(), mscale, _ROPE_LAYOUT[layout],
+                     1 if transpose else 0, _ROPE_DTYPE[x.dtype], T, H, D, rot_off, rot, out.data_ptr(), ot, oh,
+                     _current_stream(dev))
     return out
 
 
@@ -439,12 +460,14 @@ def _latent_cache(cache: torch.Tensor):
     """(dtype code, num_pages, page_size, page stride in bytes) of a paged latent cache."""
     _need(cache.dim() == 3, "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8")
     P, ps, row = cache.shape
+    stride, rs, es = cache.stride()
     fp8 = cache.dtype == torch.uint8
-    _need((fp8 and row == LATENT_ROW_BYTES) or (cache.dtype == torch.bfloat16 and row == D_QK),
+    _need((fp8 and row == LATENT_ROW_BYTES) or (row == D_QK and cache.dtype == torch.bfloat16),
           "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8")
-    _need_dense_rows(cache)
-    stride = cache.stride(0) if P > 1 else ps * row
-    return _abi.IC_FP8_E4M3 if fp8 else _abi.IC_BF16, P, ps, stride * cache.element_size()
+    _need(es == 1 and (rs == row or ps <= 1), "the rows of a page are dense")
+    if P <= 1:
+        stride = ps * row
+    return (_abi.IC_FP8_E4M3, P, ps, stride) if fp8 else (_abi.IC_BF16, P, ps, 2 * stride)
 
 
 def latent_append(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, pos: Optional[torch.Tensor] = None,
@@ -453,7 +476,11 @@ def latent_append(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, po
     """Write T latent rows kv [T, 576] bf16 into slots[t] (int64, -1 skips; slot = page * page_size + row) of the
     paged cache, quantised if it holds e4m3 rows; with pos [T] and freq [32] the 64 rotary dims are rotated as by
     ``rope``. Returns the workspace (its status word records slots outside the cache)."""
-    dev = _same_device(kv, slots, cache, pos, freq, workspace)
+    if _elsewhere(kv, stream):
+        with _on(kv, stream):
+            return latent_append(kv, slots, cache, pos, freq, layout, mscale, workspace)
+    dev = kv.get_device()
+    _same_device(dev, slots, cache, pos, freq, workspace)
     code, P, ps, stride = _latent_cache(cache)
     _need(kv.dim() == 2 and kv.shape[1] == D_QK and kv.dtype == torch.bfloat16, "kv is bf16 [T, 576]")
     T = kv.shape[0]
@@ -465,12 +492,11 @@ def latent_append(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, po
         _need(freq.shape == ((D_QK - D_V) // 2,) and freq.dtype == torch.float64, "freq is float64 [32]")
     _need(layout in _ROPE_LAYOUT, "layout is interleaved or half")
     _need_dense(slots, pos, freq)
-    with _on(dev, stream):
-        workspace = _workspace(workspace, _abi.ic_latent_append_workspace_size(), dev)
-        if T > 0:
-            _abi.ic_latent_append(_ptr(kv), kv.stride(0), _ptr(slots), _ptr(pos), _ptr(freq), float(mscale),
-                                  _ROPE_LAYOUT[layout], T, code, _ptr(cache), P, ps, stride, _ptr(workspace),
-                                  workspace.numel(), _stream_ptr())
+    workspace = _workspace(workspace, _abi.IC_STATUS_BYTES, kv.device)
+    if T > 0:
+        _abi.ic_latent_append(kv.data_ptr(), kv.stride(0), slots.data_ptr(), _addr(pos), _addr(freq), mscale,
+                              _ROPE_LAYOUT[layout], T, code, cache.data_ptr(), P, ps, stride, workspace.data_ptr(),
+                              workspace.numel(), _current_stream(dev))
     return workspace
 
 
@@ -479,46 +505,53 @@ def latent_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
     """Copy sequences out of the paged cache: rows cu_len[b] .. cu_len[b + 1] of out [R, 576] bf16 become the first
     rows of sequence b, found through block_table [B, width] int32; cu_len int64 [B + 1]. Rows behind cu_len[B] are
     left as they are."""
-    dev = _same_device(cache, block_table, cu_len, out, workspace)
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return latent_read(cache, block_table, cu_len, out, workspace)
+    dev = cache.get_device()
+    _same_device(dev, block_table, cu_len, out, workspace)
     code, P, ps, stride = _latent_cache(cache)
-    table_stride = _block_table(block_table)
-    B = block_table.shape[0]
+    B, width, table_stride = _block_table(block_table)
     _need(cu_len.shape == (B + 1,) and cu_len.dtype == torch.int64, "cu_len is int64 [B + 1]")
     _need(out.dim() == 2 and out.shape[1] == D_QK and out.dtype == torch.bfloat16, "out is bf16 [R, 576]")
     _need_dense(cu_len, out)
-    with _on(dev, stream):
-        workspace = _workspace(workspace, _abi.ic_latent_read_workspace_size(), dev)
-        if out.shape[0] > 0:
-            _abi.ic_latent_read(_ptr(cache), code, P, ps, stride, _ptr(block_table), table_stride,
-                                block_table.shape[1], _ptr(cu_len), B, _ptr(out), out.shape[0], _ptr(workspace),
-                                workspace.numel(), _stream_ptr())
+    R = out.shape[0]
+    if R > 0:
+        workspace = _workspace(workspace, _abi.IC_STATUS_BYTES, cache.device)
+        _abi.ic_latent_read(cache.data_ptr(), code, P, ps, stride, block_table.data_ptr(), table_stride, width,
+                            cu_len.data_ptr(), B, out.data_ptr(), R, workspace.data_ptr(), workspace.numel(),
+                            _current_stream(dev))
     return out
 
 
-def _block_table(table: torch.Tensor) -> int:
-    _need(table.dim() == 2 and table.dtype == torch.int32 and table.stride(1) == 1 and
-          (table.shape[0] == 1 or table.stride(0) >= table.shape[1]),
-          "block_table is int32 [B, width], dense along a row")
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+def _block_table(table: torch.Tensor):
+    """(rows, width, row stride) of a block table."""
+    _need(table.dim() == 2 and table.dtype == torch.int32, "block_table is int32 [B, width]")
+    B, width = table.shape
+    stride, one = table.stride()
+    if B <= 1:
+        stride = width
+    _need((one == 1 or width <= 1) and stride >= width, "block_table is dense along a row")
+    return B, width, stride
 
 
-def _attention_args(q, sink, gate, out, out_dtype, lse):
-    H = q.shape[-2]
-    shape = tuple(q.shape[:-1])
+def _attention_args(q, sink, gate, out, out_dtype, lse, want_lse):
+    """Checks the arguments that the two attentions share; makes the outputs that are not given."""
+    lead = q.shape[:-1]
+    wide = lead + (D_V,)
     _need(q.shape[-1] == D_QK and q.dtype == torch.bfloat16, "q is bf16 [..., H, 576]")
-    _need(sink is None or (sink.shape == (H,) and sink.dtype == torch.float32), "sink is fp32 [H]")
-    _need(gate is None or (gate.shape == shape + (D_V,) and gate.dtype == torch.bfloat16), "gate is bf16 [..., H, 512]")
-    _need(out is None or out.shape == shape + (D_V,), "out is [..., H, 512]")
-    _need((out_dtype if out is None else out.dtype) in (torch.bfloat16, torch.float32), "out is bf16 or fp32")
-    _need(lse is None or (lse.shape == shape and lse.dtype == torch.float32), "lse is fp32 [..., H]")
+    _need(sink is None or (sink.shape == lead[-1:] and sink.dtype == torch.float32), "sink is fp32 [H]")
+    _need(gate is None or (gate.shape == wide and gate.dtype == torch.bfloat16), "gate is bf16 [..., H, 512]")
     _need_dense(q, sink, gate, out, lse)
-
-
-def _attention_outputs(q, out, out_dtype, lse, want_lse):
     if out is None:
-        out = torch.empty(q.shape[:-1] + (D_V,), dtype=out_dtype, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        _need(out_dtype in _OUT_DTYPE, "out is bf16 or fp32")
+        out = torch.empty(wide, dtype=out_dtype, device=q.device)
+    else:
+        _need(out.shape == wide and out.dtype in _OUT_DTYPE, "out is [..., H, 512], bf16 or fp32")
+    if lse is not None:
+        _need(lse.shape == lead and lse.dtype == torch.float32, "lse is fp32 [..., H]")
+    elif want_lse:
+        lse = torch.empty(lead, dtype=torch.float32, device=q.device)
     return out, lse
 
 
@@ -540,27 +573,29 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     """Dense latent attention over the paged cache: q [B, H, 576] (one new token a sequence) or [B, Q, H, 576] (Q new
     tokens, token j seeing lens[b] - (Q - 1 - j) rows), block_table [B, width] int32, lens [B] int64 (0: an idle
     slot). Returns (out [..., H, 512], lse [..., H])."""
-    dev = _same_device(q, cache, block_table, lens, sink, gate, out, lse, workspace)
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return latent_decode(q, cache, block_table, lens, sink, gate, sm_scale, out_dtype, out, lse, want_lse,
+                                 workspace)
+    dev = q.get_device()
+    _same_device(dev, cache, block_table, lens, sink, gate, out, lse, workspace)
     code, P, ps, stride = _latent_cache(cache)
-    table_stride = _block_table(block_table)
+    TB, width, table_stride = _block_table(block_table)
     _need(q.dim() in (3, 4), "q is [B, H, 576] or [B, Q, H, 576]")
     B, H, Q = q.shape[0], q.shape[-2], (q.shape[1] if q.dim() == 4 else 1)
-    width = block_table.shape[1]
-    _need(block_table.shape[0] == B and lens.shape == (B,) and lens.dtype == torch.int64,
-          "block_table is [B, width], lens int64 [B]")
+    _need(TB == B and lens.shape == (B,) and lens.dtype == torch.int64, "block_table is [B, width], lens int64 [B]")
     _need_dense(lens)
-    _attention_args(q, sink, gate, out, out_dtype, lse)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(D_QK)
-    with _on(dev, stream):
-        out, lse = _attention_outputs(q, out, out_dtype, lse, want_lse)
-        if q.numel() > 0:
-            workspace = _workspace(workspace, 0 if workspace is not None else
-                                   _abi.ic_latent_decode_workspace_size(B, Q, H, width * ps), dev)
-            _abi.ic_latent_decode(_ptr(q), _ptr(cache), code, P, ps, stride, _ptr(block_table), table_stride, width,
-                                  _ptr(lens), _ptr(sink), _ptr(gate), float(sm_scale), B, Q, H,
-                                  _abi.IC_F32 if out.dtype == torch.float32 else _abi.IC_BF16, _ptr(out), _ptr(lse),
-                                  _ptr(workspace), workspace.numel(), _stream_ptr())
+    out, lse = _attention_args(q, sink, gate, out, out_dtype, lse, want_lse)
+    if B > 0 and Q > 0 and H > 0:
+        if workspace is None:
+            workspace = _workspace(None, _abi.ic_latent_decode_workspace_size(B, Q, H, width * ps), q.device)
+        else:
+            _workspace(workspace, 0, q.device)
+        _abi.ic_latent_decode(q.data_ptr(), cache.data_ptr(), code, P, ps, stride, block_table.data_ptr(),
+                              table_stride, width, lens.data_ptr(), _addr(sink), _addr(gate),
+                              _SM_SCALE if sm_scale is None else sm_scale, B, Q, H, _OUT_DTYPE[out.dtype],
+                              out.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel(),
+                              _current_stream(dev))
     return out, lse
 
 
@@ -572,26 +607,29 @@ def latent_sparse_decode(q: torch.Tensor, cache: torch.Tensor, slots: torch.Tens
     """``sparse_mla_decode`` over an e4m3 paged cache: q [B, H, 576] attends to slots [B, k] (int32, -1 padding) of
     the cache. Returns (out [B, H, 512], lse [B, H]). (Dense bf16 pages: ``sparse_mla_decode`` with
     cache.view(1, -1, 576) and the slots as idx.)"""
-    dev = _same_device(q, cache, slots, sink, gate, out, lse, workspace)
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return latent_sparse_decode(q, cache, slots, sink, gate, sm_scale, out_dtype, out, lse, want_lse,
+                                        workspace)
+    dev = q.get_device()
+    _same_device(dev, cache, slots, sink, gate, out, lse, workspace)
     code, P, ps, stride = _latent_cache(cache)
     _need(code == _abi.IC_FP8_E4M3, "the cache holds e4m3 rows")
     _need(q.dim() == 3, "q is [B, H, 576]")
     B, H, _ = q.shape
     _need(slots.dim() == 2 and slots.shape[0] == B and slots.dtype == torch.int32, "slots is int32 [B, k]")
-    _need_dense(slots)
-    _attention_args(q, sink, gate, out, out_dtype, lse)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(D_QK)
     k = slots.shape[1]
-    with _on(dev, stream):
-        out, lse = _attention_outputs(q, out, out_dtype, lse, want_lse)
-        if q.numel() > 0:
-            workspace = _workspace(workspace, 0 if workspace is not None else
-                                   _abi.ic_latent_sparse_workspace_size(B, H, k), dev)
-            _abi.ic_latent_sparse_decode(_ptr(q), _ptr(cache), P, ps, stride, _ptr(slots), k, _ptr(sink), _ptr(gate),
-                                         float(sm_scale), B, H,
-                                         _abi.IC_F32 if out.dtype == torch.float32 else _abi.IC_BF16, _ptr(out),
-                                         _ptr(lse), _ptr(workspace), workspace.numel(), _stream_ptr())
+    _need_dense(slots)
+    out, lse = _attention_args(q, sink, gate, out, out_dtype, lse, want_lse)
+    if B > 0 and H > 0:
+        if workspace is None:
+            workspace = _workspace(None, _abi.ic_latent_sparse_workspace_size(B, H, k), q.device)
+        else:
+            _workspace(workspace, 0, q.device)
+        _abi.ic_latent_sparse_decode(q.data_ptr(), cache.data_ptr(), P, ps, stride, slots.data_ptr(), k, _addr(sink),
+                                     _addr(gate), _SM_SCALE if sm_scale is None else sm_scale, B, H,
+                                     _OUT_DTYPE[out.dtype], out.data_ptr(), _addr(lse), workspace.data_ptr(),
+                                     workspace.numel(), _current_stream(dev))
     return out, lse
 
 
