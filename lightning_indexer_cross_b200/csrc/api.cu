@@ -117,7 +117,6 @@ ic_status_t indexer_impl(const void* q, const float* w, const void* k, const flo
   if (r != CUDA_SUCCESS) return IC_ERR_INVALID_ARG;
 
   ic::IndexerArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
   a.w = w;
   a.k_scale = k_scale;
   a.scale_batch_stride = per_query ? scale_batch_stride : 0;
@@ -420,7 +419,7 @@ bool paged_cache_ok(const void* cache, ic_dtype_t dtype, int64_t num_pages, int 
   return page_stride >= row * page_size && page_stride % 16 == 0;
 }
 
-// Shares of the tiles: one CTA per SM for the blocks of 64 query rows of each
+// Shares of the tiles: one CTA per SM for the blocks of 32 query rows of each
 // share, but no more shares than two-tile pieces of the longest contexts.
 int latent_groups(int64_t max_tiles, int rblocks) {
   const int64_t g = std::max(1, num_sms() / rblocks);
@@ -434,9 +433,9 @@ struct LatentLayout {
 
 LatentLayout latent_layout(int64_t B, int64_t rows, int64_t max_len) {
   LatentLayout L{};
-  L.rblocks = static_cast<int>(ceil_div<int64_t>(rows, ic::kLatentTile));
+  L.rblocks = static_cast<int>(ceil_div<int64_t>(rows, ic::kLatentRows));
   L.groups = latent_groups(B * ceil_div<int64_t>(max_len, ic::kLatentTile), L.rblocks);
-  const size_t pieces = size_t(2) * L.groups * L.rblocks * ic::kLatentTile;
+  const size_t pieces = size_t(2) * L.groups * L.rblocks * ic::kLatentRows;
   L.o_off = kStatusBytes;
   L.ml_off = align256(L.o_off + pieces * 512 * 4);
   L.total = align256(L.ml_off + pieces * 2 * 4);
@@ -469,13 +468,13 @@ ic_status_t latent_impl(const void* q, const void* cache, ic_dtype_t dtype, int6
   {
     const cuuint64_t dims[2] = {576, static_cast<cuuint64_t>(rows * B)};
     const cuuint64_t strides[1] = {576 * 2};
-    const cuuint32_t box[2] = {64, 64};
+    const cuuint32_t box[2] = {64, ic::kLatentRows};
     if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return IC_ERR_INVALID_ARG;
   }
-  CUtensorMap kvmap = qmap;  // e4m3 pages are copied without a map
+  CUtensorMap kvmap = qmap;  // e4m3 pages are read without a map
   if (!fp8) {
     const cuuint32_t br = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
     const cuuint64_t dims[3] = {576, static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(num_pages)};

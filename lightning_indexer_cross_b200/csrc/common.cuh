@@ -93,6 +93,9 @@ IC_DEV void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluste
 IC_DEV void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+IC_DEV void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 IC_DEV void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
                "r"(bytes)
@@ -155,6 +158,19 @@ IC_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, 
   }
 }
 
+// The same with little code at each place that waits: a try suspends its
+// thread for some microseconds, so nearly every wait ends in the first one, and
+// the rest is a function shared by all (a kernel of many roles is otherwise
+// bound by fetching its instructions).
+__device__ __noinline__ static bool mbar_wait_more(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                   uint64_t limit_ns) {
+  return mbar_wait(bar, parity, abort_flag, status, limit_ns);
+}
+IC_DEV bool mbar_wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+  if (limit_ns != 0 && mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_more(bar, parity, abort_flag, status, limit_ns);
+}
+
 // Wait used only while winding down after an abort: bounded, no flag check.
 IC_DEV void mbar_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
@@ -194,6 +210,10 @@ IC_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
                    smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+// Ask L2 for a contiguous range: 16-byte aligned address, bytes a multiple of 16.
+IC_DEV void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 // Shared -> global tile store of a 4-D tensor map (bulk-group completion);
 // rows outside the map's extent are not written.
@@ -265,6 +285,17 @@ IC_DEV void mma_ws_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with A in TMEM (two bf16 a column). With M = 32, lane quadrant q
+// takes its A from its own 32 lanes and holds columns [q N / 4, (q + 1) N / 4)
+// of D.
+IC_DEV void mma_ws_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // One lane of a fully active warp; the compiler then issues the lane's MMAs
 // from the uniform datapath (measured on B200: 16 to 32 cycles an issue,
 // against 96 under a lane == 0 test).
@@ -305,6 +336,24 @@ IC_DEV void tmem_ld_wait(uint32_t (&r)[32]) {
                  "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                  "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                  "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// 16 columns.
+IC_DEV void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+IC_DEV void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
@@ -436,6 +485,53 @@ IC_DEV void e4m3x16_to_bf16x16(const uint4& c, float scale, uint32_t (&o)[8]) {
     o[2 * i] = pack_bf16x2(a.x * scale, a.y * scale);
     o[2 * i + 1] = pack_bf16x2(b.x * scale, b.y * scale);
   }
+}
+
+// The same by bits, for a scale that is a power of two. Code bits seeeemmm
+// moved to s0000eeeemmm0000 are a bf16 of 2^-120 times the code's value,
+// subnormal codes included, so one multiplication by 2^120 scale finishes two
+// codes. widen_factor gives that factor twice, or kNoFactor where the scale is
+// no power of two or leaves bf16's range with 2^120; has_nan is nonzero where
+// one of the codes is 0x7f or 0xff (NaN, which the bits do not show): both then
+// need e4m3x16_to_bf16x16.
+constexpr uint32_t kNoFactor = 0xffffffffu;
+IC_DEV uint32_t widen_factor(float scale) {
+  const uint32_t sb = __float_as_uint(scale), e = sb >> 23;
+  return (sb & 0x7fffffu) == 0 && e >= 1 && e <= 134 ? (e + 120) * 0x00800080u : kNoFactor;
+}
+IC_DEV uint32_t has_nan(const uint4& c) {
+  return (((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
+          ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+}
+IC_DEV void widen16(const uint4& c, uint32_t factor, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  const __nv_bfloat162 mul = *reinterpret_cast<const __nv_bfloat162*>(&factor);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t hi = (w[i] & 0x80808080u) | ((w[i] >> 4) & 0x07070707u), lo = (w[i] << 4) & 0xf0f0f0f0u;
+    const uint32_t u0 = __byte_perm(lo, hi, 0x5140), u1 = __byte_perm(lo, hi, 0x7362);
+    const __nv_bfloat162 p0 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u0), mul);
+    const __nv_bfloat162 p1 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u1), mul);
+    o[2 * i] = *reinterpret_cast<const uint32_t*>(&p0);
+    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+  }
+}
+// The last code of `w` is read before anything that follows is issued.
+IC_DEV void use_now(uint4& w) { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)::"memory"); }
+
+// 16 bytes that no thread of the kernel writes, past L1.
+IC_DEV uint4 ld_nc_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+IC_DEV float ld_nc_f(const void* p) {
+  float v;
+  asm volatile("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
 }
 
 // ---------------------------------------------------------------- rotary angle

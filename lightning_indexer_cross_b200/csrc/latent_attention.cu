@@ -13,28 +13,39 @@
 // out evenly: group g takes tiles [g T / G, (g + 1) T / G), so ragged lengths
 // load every SM alike and a single long sequence uses all of them. The lengths
 // are read on the device; nothing waits for the host. A group has one CTA for
-// each block of 64 query rows; the CTAs of a group read the same tiles at the
+// each block of 32 query rows; the CTAs of a group read the same tiles at the
 // same time, so the second read of a tile hits L2. A piece is what one group
 // has of one sequence: whole sequences are finished by their CTA, the others
 // leave (reference, sum, unnormalised output) in fp32 and a second kernel
 // joins them.
 //
-// CTA. M = 64 query rows in the weight-stationary MMA form, whose 64 x 512
-// output takes 256 of the 512 TMEM columns (the ordinary M = 128 form would
-// need all of them and leave none for the logits). Per tile
-//   S[64 x 64]   = Q . K^T         (36 MMAs, N = 64)
+// CTA. M = 32 query rows in the weight-stationary MMA form: lane quadrant q of
+// TMEM holds the 32 rows' columns [q N / 4, (q + 1) N / 4), and Q, an operand
+// in TMEM, is there once in each quadrant. Per tile
+//   S[32 x 64]   = Q . K^T         (36 MMAs, N = 64)
 //   P            = 2^(S sm_scale log2e - ref), bf16 into shared memory
-//   O[64 x 512] += P . V           (8 MMAs, N = 256; V is the same tile read
+//   O[32 x 512] += P . V           (8 MMAs, N = 256; V is the same tile read
 //                                   as an MN-major operand)
 // with the running reference of an online softmax, moved (and O rescaled) only
 // when a row's maximum passes it by more than 2^8.
 //
-// Roles. Warp 0 finds the tiles and issues their copies, warp 1 the MMAs, warp
-// 2 loads Q, warps 4-7 run the softmax and the output. bf16 pages: TMA boxes
-// land in the operand layout; warp 3 clears the rows behind a sequence's end
-// (a zero weight times a NaN left there would be NaN). e4m3 pages: rows land
-// as they are stored and warps 8-15 widen them into the operand layout.
+// What bounds it. A tile is written to shared memory (72 KB) and read twice by
+// the MMAs (144 KB): 1720 cycles at 128 bytes a cycle. With Q in shared memory
+// too the S products would read as much again and saturate it, and every
+// mbarrier and softmax access would queue behind them; without it there is room
+// for a third tile.
+//
+// Roles. Warp 0 finds the tiles, up to kInfo ahead, and asks L2 for them;
+// warps 1 and 2 issue the two products, each as soon as its own inputs are
+// there; warps 4-7 load Q and run the softmax and the output. bf16 pages: warp
+// 3 issues TMA boxes that land in the operand layout, warp 8 clears the rows
+// behind a sequence's end (a zero weight times a NaN left there would be NaN).
+// e4m3 pages: warps 8-15 hold the next tile's codes in registers, straight from
+// L2, and widen them into the operand layout (staging them in shared memory
+// would add 84 KB to its traffic).
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -45,10 +56,13 @@ namespace {
 
 constexpr int kT = kLatentTile;
 constexpr int kSlab = kT * 128;       // 64 rows x 64 dims, bf16
-constexpr int kHalf = 4 * kSlab;      // 64 rows x 256 dims
-constexpr int kRawRows = 32;          // rows of an e4m3 staging chunk
-constexpr int kRawBytes = kRawRows * kLatentRowFp8;
-constexpr int kInfo = 8;              // tile descriptors in flight
+constexpr int kTile = 9 * kSlab;      // 64 rows of 576 dims: slabs 0-7 latent, 8 rotary
+constexpr int kStages = 3;            // tiles in shared memory
+constexpr int kClears = kStages + 1;  // as many tiles with cleared rows may be waiting for their product, and one more
+constexpr int kM = kLatentRows;       // query rows of a CTA
+constexpr int kP = kM * 128;          // 32 rows x 64 weights, bf16
+constexpr int kQSlab = kM * 128;      // 32 rows x 64 dims of Q, bf16
+constexpr uint32_t kOutCol = 0, kSCol = 128, kQCol = 160;  // TMEM columns: 128 of O, 2 x 16 of S, 288 of Q
 constexpr int kMinTiles = 2;          // tiles of a group, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.f;          // log2 units by which a row's maximum may pass its reference
@@ -58,33 +72,28 @@ struct TileInfo {
   int b, pos0, len, flags;
   uint32_t mask[2];  // valid rows of the tile
   int slot;          // partial slot of the piece
-  int pad;
+  int row0;          // bf16: row of the tile's first position within its page
+  int64_t at[4];     // dense: byte offset of each 16 rows (e4m3), or page of each box (bf16; -1: none)
 };
 
-template <bool FP8>
+template <bool FP8, bool SPARSE>
 struct Cfg {
-  static constexpr int kThreads = FP8 ? 512 : 256;
-  static constexpr int kHalves = FP8 ? 2 : 4;  // 32 KB operand slots (latent halves of a tile)
-  static constexpr int kRopes = 2;             // 8 KB operand slots (rotary slab of a tile)
-  static constexpr int kRaws = FP8 ? 3 : 1;             // e4m3 staging chunks (bf16: none used)
-  // QK of a tile is issued before PV of the previous one; needs two tiles of operand slots
-  static constexpr int kLag = FP8 ? 0 : 1;
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffHalf = 9 * kSlab;
-  static constexpr int kOffRope = kOffHalf + kHalves * kHalf;
-  static constexpr int kOffP = kOffRope + kRopes * kSlab;
-  static constexpr int kOffRaw = kOffP + kSlab;
-  static constexpr int kOffX = kOffRaw + (FP8 ? kRaws * kRawBytes : 0);  // [2][128] row maxima / sums
+  static constexpr int kThreads = FP8 ? 512 : 288;
+  // tile descriptors in flight; a sparse one has its 64 rows' places with it
+  static constexpr int kInfo = SPARSE ? 3 : 8;
+  static constexpr int kOffP = kStages * kTile;  // [2] weights of a tile
+  static constexpr int kOffX = kOffP + 2 * kP;  // [2][128] row maxima / sums
   static constexpr int kOffInfo = kOffX + 2 * 128 * 4;
-  static constexpr int kOffBar = kOffInfo + kInfo * static_cast<int>(sizeof(TileInfo));
-  // readers of a tile descriptor: MMA, Q, four softmax warps, the clearing warp or the widening warps
-  static constexpr int kReaders = 6 + (FP8 ? 8 : 1);
-  static constexpr int kNumBars = 2 * kInfo + 2 * kHalves + 2 * kRopes + 2 * kRaws + 10;
+  static constexpr int kOffSlots = kOffInfo + kInfo * static_cast<int>(sizeof(TileInfo));
+  static constexpr int kOffBar = kOffSlots + (SPARSE ? kInfo * kT * 8 : 0);
+  // readers of a tile descriptor: the two issuing warps, four softmax warps, and
+  // the copying and the clearing warp or the widening warps
+  static constexpr int kReaders = 6 + (FP8 ? 8 : 2);
+  static constexpr int kNumBars = 2 * kInfo + 2 * kStages + 11 + kClears;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16;
-  static_assert(kOffBar % 8 == 0 && kOffRaw % 128 == 0, "alignment");
+  static_assert(kOffBar % 8 == 0, "alignment");
   static_assert(kSmemBytes <= 232448, "fits one CTA per SM");
-  static_assert(kLag == 0 || (kHalves >= 4 && kRopes >= 2), "slots of two tiles");
 };
 
 IC_DEV int64_t clamp_len(const LatentArgs& a, int64_t n) {
@@ -103,39 +112,34 @@ IC_DEV int eff_groups(int groups, int64_t tiles) {
 }
 
 template <bool FP8, bool SPARSE>
-__global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     latent_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
                             const LatentArgs a) {
-  using C = Cfg<FP8>;
+  using C = Cfg<FP8, SPARSE>;
+  constexpr int kInfo = C::kInfo;
   extern __shared__ __align__(1024) uint8_t smem[];
   // the swizzled layouts need a 1024-byte-aligned base
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_status(a.status, IC_ERR_UNSUPPORTED);
     return;
   }
-  uint8_t* qs = smem + C::kOffQ;
-  uint8_t* halves = smem + C::kOffHalf;
-  uint8_t* ropes = smem + C::kOffRope;
   uint8_t* ps = smem + C::kOffP;
-  uint8_t* raws = smem + C::kOffRaw;
   float* xm = reinterpret_cast<float*>(smem + C::kOffX);
   TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kOffInfo);
+  int64_t* places = reinterpret_cast<int64_t*>(smem + C::kOffSlots);  // sparse: [kInfo][64] byte offsets in the cache
   uint64_t* info_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* info_free = info_full + kInfo;
-  uint64_t* half_full = info_free + kInfo;
-  uint64_t* half_free = half_full + C::kHalves;
-  uint64_t* rope_full = half_free + C::kHalves;
-  uint64_t* rope_free = rope_full + C::kRopes;
-  uint64_t* raw_full = rope_free + C::kRopes;
-  uint64_t* raw_free = raw_full + C::kRaws;
-  uint64_t* q_full = raw_free + C::kRaws;
-  uint64_t* q_free = q_full + 1;   // the piece's last QK has read Q
-  uint64_t* s_full = q_free + 1;   // [2] logits of a tile in TMEM
-  uint64_t* p_ready = s_full + 2;  // weights of a tile in shared memory, O rescaled
-  uint64_t* pv_done = p_ready + 1;
-  uint64_t* o_free = pv_done + 1;  // a piece's output has been read out
-  uint64_t* cleared = o_free + 1;  // bf16: the rows behind the end are zero
-  uint64_t* xch = cleared + 1;     // softmax threads exchange a value
+  // the stages hold, in order, each piece's Q and its tiles
+  uint64_t* full = info_free + kInfo;  // [kStages] Q as loaded, or a tile in operand layout
+  uint64_t* freed = full + kStages;    // [kStages] Q is in TMEM, or the tile's last product has read it (bf16: and warp 8 has seen it)
+  uint64_t* q_full = freed + kStages;
+  uint64_t* q_free = q_full + 1;    // the piece's last QK has read Q
+  uint64_t* s_full = q_free + 1;    // [2] logits of a tile in TMEM
+  uint64_t* p_ready = s_full + 2;   // [2] weights of a tile in shared memory, its logits read, O rescaled
+  uint64_t* pv_done = p_ready + 2;  // [2]
+  uint64_t* o_free = pv_done + 2;   // a piece's output has been read out
+  uint64_t* cleared = o_free + 1;   // [kClears] bf16: a tile's rows that hold nothing are zero
+  uint64_t* xch = cleared + kClears;  // the softmax warps exchange a value
   uint64_t* retire = xch + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -150,28 +154,21 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
       mbar_init(&info_full[i], 1);
       mbar_init(&info_free[i], C::kReaders);
     }
-    for (int i = 0; i < C::kHalves; ++i) {
-      mbar_init(&half_full[i], FP8 ? 128 : 1);
-      mbar_init(&half_free[i], 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], FP8 ? 8 : 1);
+      mbar_init(&freed[i], FP8 ? 1 : 2);
     }
-    for (int i = 0; i < C::kRopes; ++i) {
-      mbar_init(&rope_full[i], FP8 ? 256 : 1);
-      mbar_init(&rope_free[i], 1);
-    }
-    for (int i = 0; i < C::kRaws; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_free[i], 256);
-    }
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 4);
     mbar_init(q_free, 1);
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(p_ready, 128);
-    mbar_init(pv_done, 1);
-    mbar_init(o_free, 128);
-    mbar_init(cleared, 32);
-    mbar_init(xch, 128);
-    mbar_init(retire, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(o_free, 4);
+    for (int i = 0; i < kClears; ++i) mbar_init(&cleared[i], 1);
+    mbar_init(xch, 4);
+    mbar_init(retire, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -184,11 +181,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t kOutCol = 0, kSCol = 256;
   // one thread's wait, and a whole warp's: its lanes leave a wait that was
   // given up together, so that no lane stays behind in a warp-wide instruction
-  auto wait1 = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.status, a.wait_ns); };
+  auto wait1 = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_hot(bar, parity, abort_flag, a.status, a.wait_ns); };
   auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait1(bar, parity)) != 0; };
+  // one arrival for the warp, after all its lanes' writes. (The lanes meet
+  // again before any of them can enter a wait: a try suspends the warp, and the
+  // one lane's work would wait with it.)
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    __syncwarp();
+  };
   // the descriptor of tile t, read by one thread or by a whole warp
   auto get_info1 = [&](int t, TileInfo& x) {
     if (!wait1(&info_full[t % kInfo], (t / kInfo) & 1)) return false;
@@ -199,13 +203,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
   auto get_info = [&](int t, TileInfo& x) {
     if (!wait(&info_full[t % kInfo], (t / kInfo) & 1)) return false;
     x = infos[t % kInfo];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&info_free[t % kInfo]);
+    warp_arrive(&info_free[t % kInfo]);
     return true;
   };
+  // slab c of Q's rows of sequence b into a stage. (Rows of the next sequence, or
+  // zeros, may lie behind this one's: they are not written out.)
+  auto copy_q = [&](int b, int st, int c) {
+    tma_load_2d(smem + st * kTile + c * kQSlab, &qmap, &full[st], c * 64, b * a.rows + rb * kM);
+  };
+  const int br = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;  // rows of a TMA box
 
   if (warp == 0) {
-    // ------------------------------------------------------------ tiles and their copies
+    // ------------------------------------------------------------ tiles
     // this group's share of all tiles
     int64_t total = 0;
     if (SPARSE) {
@@ -258,11 +267,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
       }
     }
     int n = static_cast<int>(g1 - g0);
-    const int br = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;  // rows of a TMA box
-    const int run = br < kRawRows ? br : kRawRows;                                // rows of an e4m3 copy
+    const int unit = FP8 ? 16 : br;  // rows of an entry of page[]
     bool ok = true;
     int t = 0;
-    int raw = 0, nrope = 0, nhalf = 0;  // e4m3 chunks, rotary slabs, latent halves issued
     for (; t < n && ok; ++t) {
       const int64_t gt = g0 + t;
       while (gt >= bstart + bt && b + 1 < a.B) {  // the next sequence with tiles
@@ -282,13 +289,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
       const int pos0 = static_cast<int>(gt - bstart) * kT;
       const bool first = t == 0 || gt == bstart;
       const bool last = t == n - 1 || gt == bstart + bt - 1;
-      // where the rows are: lane l finds the box (or copy, or row) l of the tile
-      int64_t src = -1;   // e4m3: byte offset of the copy's first row
-      int src_page = -1;  // bf16: page of the box
-      int rows = 0;       // valid rows of the box
-      int64_t src2 = -1;  // sparse: row 32 + lane
-      const int unit = FP8 ? run : br;
       uint32_t m0 = 0, m1 = 0;
+      int64_t s0 = -1, s1 = -1;  // sparse: this lane's two rows
+      int64_t src = FP8 ? 0 : -1;  // dense: lane l has the place of the tile's l-th unit
       if constexpr (SPARSE) {
         const int64_t num = static_cast<int64_t>(a.num_pages) * a.page_size;
         auto find = [&](int j) -> int64_t {
@@ -299,26 +302,31 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             return -1;
           }
           const int page = s / a.page_size;
-          return page * a.page_stride + static_cast<int64_t>(s - page * a.page_size) * kLatentRowFp8;
+          const int64_t at = page * a.page_stride + static_cast<int64_t>(s - page * a.page_size) * kLatentRowFp8;
+          bulk_prefetch_l2(a.cache + at, kLatentRowFp8);
+          return at;
         };
-        src = find(pos0 + lane);
-        src2 = find(pos0 + 32 + lane);
-        m0 = __ballot_sync(0xffffffffu, src >= 0);
-        m1 = __ballot_sync(0xffffffffu, src2 >= 0);
+        s0 = find(pos0 + lane);
+        s1 = find(pos0 + 32 + lane);
+        m0 = __ballot_sync(0xffffffffu, s0 >= 0);
+        m1 = __ballot_sync(0xffffffffu, s1 >= 0);
       } else {
         const int p = pos0 + lane * unit;
+        int rows = 0;  // valid rows of the unit
         if (lane * unit < kT && p < blen) {
           const int pi = p / a.page_size;
           const int page = a.table[static_cast<int64_t>(b) * a.table_stride + pi];
           if (page >= 0 && page < a.num_pages) {
             rows = blen - p < unit ? blen - p : unit;
-            src_page = page;
-            src = page * a.page_stride + static_cast<int64_t>(p - pi * a.page_size) * kLatentRowFp8;
+            constexpr int kRow = FP8 ? kLatentRowFp8 : kLatentRowBf16;
+            const int64_t byte = page * a.page_stride + static_cast<int64_t>(p - pi * a.page_size) * kRow;
+            src = FP8 ? byte : page;
+            bulk_prefetch_l2(a.cache + byte, static_cast<uint32_t>(rows * kRow));
           } else {
             record_status(a.status, IC_ERR_BAD_INDEX);
           }
         }
-        // bit r of the mask: row r is in a valid box, before the end
+        // bit r of the mask: row r is in a valid unit, before the end
         const int rows_of = __shfl_sync(0xffffffffu, rows, lane / unit);
         const int rows_of2 = __shfl_sync(0xffffffffu, rows, (32 + lane) / unit);
         m0 = __ballot_sync(0xffffffffu, lane % unit < rows_of);
@@ -328,10 +336,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         ok = false;
         break;
       }
+      TileInfo& x = infos[t % kInfo];
+      if constexpr (SPARSE) {
+        places[(t % kInfo) * kT + lane] = s0;
+        places[(t % kInfo) * kT + 32 + lane] = s1;
+      } else {
+        if (lane < 4) x.at[lane] = src;
+      }
+      __syncwarp();
       if (lane == 0) {
-        TileInfo& x = infos[t % kInfo];
         x.b = b;
         x.pos0 = pos0;
+        x.row0 = SPARSE ? 0 : pos0 % a.page_size;
         x.len = blen;
         x.mask[0] = m0;
         x.mask[1] = m1;
@@ -341,150 +357,42 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                   (bstart >= g0 && bstart + bt <= g1 ? kWhole : 0) | ((m0 & m1) != 0xffffffffu ? kClear : 0);
         mbar_arrive(&info_full[t % kInfo]);
       }
-      if constexpr (FP8) {
-        for (int c = 0; c < 2; ++c, ++raw) {
-          const int rs = raw % C::kRaws;
-          if (!wait(&raw_free[rs], ((raw / C::kRaws) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = raws + rs * kRawBytes;
-          const uint32_t bytes = static_cast<uint32_t>(__popc(c ? m1 : m0)) * kLatentRowFp8;
-          if (lane == 0) {
-            if (bytes) mbar_arrive_expect_tx(&raw_full[rs], bytes);
-            else mbar_arrive(&raw_full[rs]);
-          }
-          __syncwarp();
-          if constexpr (SPARSE) {
-            const int64_t s = c ? src2 : src;
-            if (s >= 0) bulk_load(dst + lane * kLatentRowFp8, a.cache + s, kLatentRowFp8, &raw_full[rs]);
-          } else {
-            const int l0 = c * (kRawRows / unit);  // lanes [l0, l0 + 32 / unit) have this chunk's copies
-            if (lane >= l0 && lane < l0 + kRawRows / unit && rows > 0)
-              bulk_load(dst + (lane - l0) * unit * kLatentRowFp8, a.cache + src,
-                        static_cast<uint32_t>(rows) * kLatentRowFp8, &raw_full[rs]);
-          }
-        }
-      } else {
-        // boxes without a valid row read the page behind the last, which fills zeros
-        const int pz = src_page >= 0 ? src_page : a.num_pages;
-        const int py = (pos0 + lane * br) % a.page_size;
-        const int rs = t % C::kRopes;
-        if (!wait(&rope_free[rs], ((t / C::kRopes) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&rope_full[rs], kSlab);
-        __syncwarp();
-        ++nrope;
-        if (lane * br < kT) tma_load_3d(ropes + rs * kSlab + lane * br * 128, &kvmap, &rope_full[rs], 512, py, pz);
-        for (int h = 0; h < 2; ++h) {
-          const int hc = 2 * t + h, hs = hc % C::kHalves;
-          if (!wait(&half_free[hs], ((hc / C::kHalves) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&half_full[hs], kHalf);
-          __syncwarp();
-          ++nhalf;
-          if (lane * br < kT)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tma_load_3d(halves + hs * kHalf + c * kSlab + lane * br * 128, &kvmap, &half_full[hs], h * 256 + c * 64,
-                          py, pz);
-        }
-      }
+      __syncwarp();
     }
     if (ok) ok = wait(&info_free[n % kInfo], ((n / kInfo) & 1) ^ 1);
     if (ok && lane == 0) {
       infos[n % kInfo].flags = kEnd;
       mbar_arrive(&info_full[n % kInfo]);
     }
-    // the last copies of each slot land before the CTA exits, whatever their readers do
-    for (int u = raw > C::kRaws ? raw - C::kRaws : 0; u < raw; ++u)
-      mbar_drain(&raw_full[u % C::kRaws], (u / C::kRaws) & 1);
-    for (int u = nrope > C::kRopes ? nrope - C::kRopes : 0; u < nrope; ++u)
-      mbar_drain(&rope_full[u % C::kRopes], (u / C::kRopes) & 1);
-    for (int u = nhalf > C::kHalves ? nhalf - C::kHalves : 0; u < nhalf; ++u)
-      mbar_drain(&half_full[u % C::kHalves], (u / C::kHalves) & 1);
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs
+    // ------------------------------------------------------------ S = Q . K^T
     if (elect_one()) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(64, 64, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(64, 256, false, true);
-      const uint32_t qa = smem_u32(qs), ha = smem_u32(halves), ra = smem_u32(ropes), pa = smem_u32(ps);
-      int piece = -1, nclear = 0;  // piece of the tile whose PV comes next; cleared tiles seen
-      // O += P . V of tile t
-      auto pv = [&](int t, bool first) {
-        if (first) {
-          ++piece;
-          if (piece > 0 && !wait1(o_free, (piece - 1) & 1)) return false;
+      constexpr uint32_t idesc = idesc_bf16_f32(kM, kT, false, false);
+      const uint32_t ka = smem_u32(smem);
+      int pieces = 0, n = 0;  // stages used so far
+      for (int t = 0;; ++t, ++n) {
+        TileInfo x;
+        if (!get_info1(t, x) || (x.flags & kEnd)) break;
+        if (x.flags & kFirst) {
+          if (!wait1(q_full, pieces & 1)) break;
+          mbar_arrive(&freed[n % kStages]);
+          ++pieces;
+          ++n;
         }
-        if (!wait1(p_ready, t & 1)) return false;
+        // the logits of tile t - 2 have been read
+        if (t >= 2 && !wait1(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
+        const int st = n % kStages;
+        if (!wait1(&full[st], (n / kStages) & 1)) break;
         tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t hs = (2 * t + h) % C::kHalves;
-          const uint64_t vd = sw128_desc(ha + hs * kHalf, kSlab, 1024), pd = sw128_desc(pa, 16, 1024);
+        const uint32_t d = tmem + kSCol + (t & 1) * 16;
+        const uint64_t bd = sw128_desc(ka + st * kTile, 16, 1024);
+#pragma unroll 1
+        for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ws_bf16_ss(tmem + kOutCol + h * 128, pd + kk * 2, vd + kk * 128, idesc_pv, !first || kk > 0);
-          mma_commit(&half_free[hs]);
-        }
-        mma_commit(pv_done);
-        return true;
-      };
-      int npieces = 0;
-      bool prev_first = false;
-      for (int t = 0;; ++t) {
-        TileInfo x;
-        if (!get_info1(t, x)) break;
-        const bool end = (x.flags & kEnd) != 0, first = (x.flags & kFirst) != 0;
-        // a piece's first QK waits for its Q, which is loaded once the last
-        // piece's QK is done: that piece's last PV goes first
-        if (C::kLag && t > 0 && (end || first) && !pv(t - 1, prev_first)) break;
-        if (end) break;
-        if (first) {
-          if (!wait1(q_full, npieces & 1)) break;
-          ++npieces;
-        }
-        if (!FP8 && (x.flags & kClear)) {
-          if (!wait1(cleared, nclear & 1)) break;
-          ++nclear;
-        }
-        const uint32_t d = tmem + kSCol + (t & 1) * 32;
-        const int rs = t % C::kRopes;
-        if (!wait1(&rope_full[rs], (t / C::kRopes) & 1)) break;
-        tc_fence_after();
-        {
-          const uint64_t ad = sw128_desc(qa + 8 * kSlab, 16, 1024), bd = sw128_desc(ra + rs * kSlab, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ws_bf16_ss(d, ad + kk * 2, bd + kk * 2, idesc_qk, kk > 0);
-          mma_commit(&rope_free[rs]);
-        }
-        bool ok = true;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int hc = 2 * t + h, hs = hc % C::kHalves;
-          if (ok && !wait1(&half_full[hs], (hc / C::kHalves) & 1)) ok = false;
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = sw128_desc(qa + h * 4 * kSlab, 16, 1024), bd = sw128_desc(ha + hs * kHalf, 16, 1024);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ws_bf16_ss(d, ad + c * (kSlab >> 4) + kk * 2, bd + c * (kSlab >> 4) + kk * 2, idesc_qk, 1);
-        }
-        if (!ok) break;
+            mma_ws_bf16_ts(d, tmem + kQCol + c * 32 + kk * 8, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
         mma_commit(&s_full[t & 1]);
         if (x.flags & kLast) mma_commit(q_free);
-        if (C::kLag) {
-          if (t > 0 && !first && !pv(t - 1, prev_first)) break;
-          prev_first = first;
-        } else if (!pv(t, first)) {
-          break;
-        }
       }
       // every MMA issued has retired before TMEM is released
       mma_commit(retire);
@@ -492,126 +400,205 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ------------------------------------------------------------ Q of each piece
-    if (lane == 0) {
-      int piece = 0;
-      for (int t = 0;; ++t) {
+    // ------------------------------------------------------------ O += P . V
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kM, 256, false, true);
+      const uint32_t va = smem_u32(smem), pa = smem_u32(ps);
+      int pieces = 0, nclear = 0, n = 0;
+      for (int t = 0;; ++t, ++n) {
         TileInfo x;
         if (!get_info1(t, x) || (x.flags & kEnd)) break;
-        if (!(x.flags & kFirst)) continue;
-        if (piece > 0 && !wait1(q_free, (piece - 1) & 1)) break;
-        mbar_arrive_expect_tx(q_full, 9 * kSlab);
-        const int row = x.b * a.rows + rb * 64;  // rows of the next sequence, or zeros, behind this one's: not written out
-        for (int c = 0; c < 9; ++c) tma_load_2d(qs + c * kSlab, &qmap, q_full, c * 64, row);
-        ++piece;
+        const bool first = (x.flags & kFirst) != 0;
+        if (first) {
+          if (pieces > 0 && !wait1(o_free, (pieces - 1) & 1)) break;
+          ++pieces;
+          ++n;
+        }
+        if (!FP8 && (x.flags & kClear)) {
+          if (!wait1(&cleared[nclear % kClears], (nclear / kClears) & 1)) break;
+          ++nclear;
+        }
+        const int st = n % kStages;
+        if (!wait1(&full[st], (n / kStages) & 1)) break;
+        if (!wait1(&p_ready[t & 1], (t >> 1) & 1)) break;
+        tc_fence_after();
+        const uint64_t vd = sw128_desc(va + st * kTile, kSlab, 1024), pd = sw128_desc(pa + (t & 1) * kP, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma_ws_bf16_ss(tmem + kOutCol + h * 64, pd + kk * 2, vd + h * (4 * kSlab >> 4) + kk * 128, idesc,
+                           !first || kk > 0);
+        mma_commit(&freed[st]);
+        mma_commit(&pv_done[t & 1]);
       }
-      if (piece > 0) mbar_drain(q_full, (piece - 1) & 1);
+      mma_commit(retire);
+      mbar_drain(retire, 0);
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ------------------------------------------------------------ rows behind the end (bf16)
+    // ------------------------------------------------------------ copies (bf16)
+    // The stages have one producer that fills them in order: a second one that
+    // ran ahead would take the parity of an older phase for its own.
     if (!FP8) {
+      int n = 0;
+      auto stage = [&](uint32_t bytes) {  // the next stage, ready for copies of so many bytes
+        if (!wait(&freed[n % kStages], ((n / kStages) & 1) ^ 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&full[n % kStages], bytes);
+        __syncwarp();
+        return true;
+      };
       for (int t = 0;; ++t) {
         TileInfo x;
-        bool ok = get_info(t, x);
-        if (!ok || (x.flags & kEnd)) break;
-        if (!(x.flags & kClear)) continue;
-        for (int h = 0; h < 2 && ok; ++h) {
-          const int hc = 2 * t + h, hs = hc % C::kHalves;
-          ok = wait(&half_full[hs], (hc / C::kHalves) & 1);
-          if (!ok) break;
-          const uint32_t base = smem_u32(halves + hs * kHalf) + (lane >> 3) * kSlab + (lane & 7) * 16;
-          for (int r = 0; r < kT; ++r)
-            if (!((x.mask[r >> 5] >> (r & 31)) & 1u)) st_shared_v4(base + r * 128, make_uint4(0, 0, 0, 0));
+        if (!get_info(t, x) || (x.flags & kEnd)) break;
+        if (x.flags & kFirst) {
+          if (!stage(9 * kQSlab)) break;
+          if (lane < 9) copy_q(x.b, n % kStages, lane);
+          __syncwarp();
+          ++n;
         }
-        if (!ok) break;
-        fence_proxy_async_smem();
-        mbar_arrive(cleared);
+        if (!stage(kTile)) break;
+        // lane l has box l of each slab; boxes without a valid row read the
+        // page behind the last, which fills zeros
+        const int64_t page = lane == 0 ? x.at[0] : lane == 1 ? x.at[1] : lane == 2 ? x.at[2] : x.at[3];
+        const int pz = page < 0 ? a.num_pages : static_cast<int>(page);
+        const int py = (x.row0 + lane * br) % a.page_size;
+        if (lane * br < kT)
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c)
+            tma_load_3d(smem + (n % kStages) * kTile + c * kSlab + lane * br * 128, &kvmap, &full[n % kStages], c * 64,
+                        py, pz);
+        __syncwarp();
+        ++n;
       }
+      // the last copies of each stage land before the CTA exits, whatever their readers do
+      for (int u = n > kStages ? n - kStages : 0; u < n; ++u)
+        if (lane == 0) mbar_drain(&full[u % kStages], (u / kStages) & 1);
+      __syncwarp();
     }
   } else if (warp < 8) {
-    // ------------------------------------------------------------ softmax and output
-    // Thread (quadrant, lane) has query row r of the block and one half of the
-    // columns: 32 of a tile's keys, 256 of the output dims.
-    const int quad = warp & 3, colh = quad >> 1;
-    const int r = (quad & 1) * 32 + lane;
-    const int tid = quad * 32 + lane;
+    // ------------------------------------------------------------ Q, softmax and output
+    // Thread (quadrant, lane) has query row `lane` of the block and a quarter
+    // of the columns: 16 of a tile's keys, 128 of the output dims.
+    const int quad = warp & 3;
     const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float c2 = a.sm_scale * kLog2e;
-    const int row = rb * 64 + r;             // query row of the sequence
+    const int row = rb * kM + lane;          // query row of the sequence
     const bool live = row < a.rows;
     const int back = a.Q - 1 - (live ? row / a.H : 0);  // the row's token ends this many positions before the last
     const float sink2 = a.sink && live ? a.sink[row % a.H] * kLog2e : -INFINITY;
     float ref = -INFINITY, l = 0.f;
     uint32_t nx = 0;  // exchanges so far
-    auto exchange = [&](float v, float& other) {
-      float* buf = xm + (nx & 1) * 128;
-      buf[tid] = v;
-      mbar_arrive(xch);
+    auto offer = [&](float v) {
+      xm[(nx & 1) * 128 + quad * 32 + lane] = v;
+      warp_arrive(xch);
+    };
+    auto take = [&](float (&v)[4]) {
       const bool ok = wait(xch, nx & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = xm[(nx & 1) * 128 + i * 32 + lane];
       ++nx;
-      other = buf[tid ^ 64];
       return ok;
     };
-    for (int t = 0;; ++t) {
-      TileInfo x;
-      bool ok = get_info(t, x);
-      if (!ok || (x.flags & kEnd)) break;
+    // Q of a piece from its stage into the quadrant's copy in TMEM
+    int n = 0;
+    auto load_q = [&]() {
+      if (!wait(&full[n % kStages], (n / kStages) & 1)) return false;
+      const uint8_t* src = smem + (n % kStages) * kTile;
+#pragma unroll 1
+      for (int c = 0; c < 9; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(src + c * kQSlab + sw128_offset(lane, i));
+          v[4 * i] = w.x;
+          v[4 * i + 1] = w.y;
+          v[4 * i + 2] = w.z;
+          v[4 * i + 3] = w.w;
+        }
+        tmem_st32(tlane + kQCol + c * 32, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(q_full);
+      ++n;
+      return true;
+    };
+    TileInfo x;
+    int pieces = 0;
+    bool ok = get_info(0, x);
+    if (ok && !(x.flags & kEnd)) ok = load_q();
+    for (int t = 0; ok && !(x.flags & kEnd); ++t) {
+      ++n;
       ok = wait(&s_full[t & 1], (t >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t rv[32];
-      tmem_ld32_issue(tlane + kSCol + (t & 1) * 32, rv);
+      uint32_t rv[16];
+      tmem_ld16_issue(tlane + kSCol + (t & 1) * 16, rv);
       if (x.flags & kFirst) {
         ref = -INFINITY;
         l = 0.f;
       }
-      uint32_t mask = x.mask[colh];
-      const int seen = x.len - back - (x.pos0 + colh * 32);  // columns of this thread before the row's limit
-      if (seen < 32) mask = seen <= 0 ? 0u : mask & ((1u << seen) - 1);
-      tmem_ld_wait(rv);
-      if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
+      uint32_t mask = ((quad & 2 ? x.mask[1] : x.mask[0]) >> ((quad & 1) * 16)) & 0xffffu;
+      const int seen = x.len - back - (x.pos0 + quad * 16);  // columns of this thread before the row's limit
+      if (seen < 16) mask = seen <= 0 ? 0u : mask & ((1u << seen) - 1);
+      tmem_ld_wait16(rv);
+      if (!__all_sync(0xffffffffu, mask == 0xffffu)) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
           if (!((mask >> j) & 1u)) rv[j] = 0xff800000u;  // -inf
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(rv[j]));
-      const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      float other;
-      ok = exchange(mine, other);
+      for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(rv[j]));
+      offer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      // The sum is of the 32-bit weights; those of the product are rounded to
+      // bf16 (2^-8 of each at most, of either sign), as the MMA takes them.
+      uint32_t pk[8];
+      float sum = 0.f;
+      auto weigh = [&](float base) {
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(rv[j]), c2, -base));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(rv[j + 1]), c2, -base));
+          part[(j >> 1) & 3] += p0 + p1;
+          pk[j >> 1] = pack_bf16x2(p0, p1);
+        }
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
+      };
+      // weights under the old reference, while the other quarters' maxima
+      // come: most tiles leave it where it is
+      const bool early = __any_sync(0xffffffffu, ref != -INFINITY) != 0;
+      if (early) weigh(ref == -INFINITY ? 0.f : ref);
+      float other[4];
+      ok = take(other);
       if (!ok) break;
-      const float m = fmaxf(mine, other) * c2;
+      const float m = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3])) * c2;
       // the reference moves when the row's maximum passes it by more than
       // kMove: weights stay below 2^8, far from bf16's and fp32's limits
       float scale = 1.f;
+      bool moved = false;
       if (ref == -INFINITY) {
+        moved = m != -INFINITY;
         ref = m;
       } else if (m > ref + kMove) {
         scale = ex2_approx(ref - m);
         ref = m;
+        moved = true;
       }
-      const float base = ref == -INFINITY ? 0.f : ref;  // nothing valid so far: every weight is 0
-      uint32_t pk[16];
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      // the sum is of the 32-bit weights; those of the product are rounded to
-      // bf16 (2^-8 of each at most, of either sign), as the MMA takes them
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float p0 = ex2_approx(fmaf(__uint_as_float(rv[j]), c2, -base));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(rv[j + 1]), c2, -base));
-        sum[(j >> 1) & 3] += p0 + p1;
-        pk[j >> 1] = pack_bf16x2(p0, p1);
-      }
-      l = fmaf(l, scale, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-      // the previous PV has read the weights, and O stands still
-      if (t > 0) ok = wait(pv_done, (t - 1) & 1);
+      // (a row with nothing valid so far: every weight is 0)
+      if (!early || __any_sync(0xffffffffu, moved)) weigh(ref == -INFINITY ? 0.f : ref);
+      l = fmaf(l, scale, sum);
+      // the product of two tiles ago has read its weights
+      if (t >= 2) ok = wait(&pv_done[t & 1], ((t >> 1) - 1) & 1);
       if (!ok) break;
-      if (__any_sync(0xffffffffu, scale != 1.f)) {
+      if (__any_sync(0xffffffffu, scale != 1.f)) {  // (then t > 0, and the four warps agree)
+        ok = wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);  // O stands still
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
           tmem_ld32_issue(tlane + kOutCol + c * 32, o);
           tmem_ld_wait(o);
@@ -621,41 +608,53 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         }
         tmem_st_wait();
       }
-      const uint32_t pb = smem_u32(ps);
+      const uint32_t pb = smem_u32(ps + (t & 1) * kP);
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4)
-        st_shared_v4(pb + sw128_offset(r, colh * 4 + q4),
-                     make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]));
+      for (int i = 0; i < 2; ++i)
+        st_shared_v4(pb + sw128_offset(lane, quad * 2 + i),
+                     make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(p_ready);
-      if (!(x.flags & kLast)) continue;
-      // ---- the piece's output
-      float l2;
-      ok = exchange(l, l2) && wait(pv_done, t & 1);
+      warp_arrive(&p_ready[t & 1]);
+      TileInfo y = x;
+      ok = get_info(t + 1, x);
+      if (!ok) break;
+      if (!(y.flags & kLast)) continue;
+      // ---- Q of the next piece, and this one's output
+      if (!(x.flags & kEnd)) {
+        ok = wait(q_free, pieces & 1);
+        if (!ok) break;
+        tc_fence_after();
+        ok = load_q();
+        if (!ok) break;
+      }
+      ++pieces;
+      offer(l);
+      float ls[4];
+      ok = take(ls) && wait(&pv_done[t & 1], (t >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const float lsum = l + l2;
-      const bool whole = (x.flags & kWhole) != 0;
-      const int64_t gr = (static_cast<int64_t>(x.b) * a.rows) + row;
-      const int64_t pr = (static_cast<int64_t>(x.slot) * a.rblocks + rb) * 64 + r;
+      const float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      const bool whole = (y.flags & kWhole) != 0;
+      const int64_t gr = (static_cast<int64_t>(y.b) * a.rows) + row;
+      const int64_t pr = (static_cast<int64_t>(y.slot) * a.rblocks + rb) * kM + lane;
       float f = 1.f;
       if (whole) {
         const float M = fmaxf(ref, sink2);
         const float w = ref == -INFINITY ? 0.f : exp2f(ref - M);
         const float den = lsum * w + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - M));
         f = w > 0.f ? w / den : 0.f;
-        if (live && colh == 0 && a.lse) a.lse[gr] = M == -INFINITY ? -INFINITY : (M + log2f(den)) / kLog2e;
-      } else if (colh == 0) {
+        if (live && quad == 0 && a.lse) a.lse[gr] = M == -INFINITY ? -INFINITY : (M + log2f(den)) / kLog2e;
+      } else if (quad == 0) {
         a.part_ml[pr * 2] = ref;
         a.part_ml[pr * 2 + 1] = lsum;
       }
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         tmem_ld32_issue(tlane + kOutCol + c * 32, o);
         tmem_ld_wait(o);
-        const int dim = (c >> 2) * 256 + colh * 128 + (c & 3) * 32;
+        const int dim = (c >> 1) * 256 + quad * 64 + (c & 1) * 32;
         if (!whole) {
           uint4* dst = reinterpret_cast<uint4*>(a.part_o + pr * 512 + dim);
 #pragma unroll
@@ -693,55 +692,183 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(o_free);
+      warp_arrive(o_free);
     }
-  } else if (FP8) {
-    // ------------------------------------------------------------ widening (e4m3)
-    // Warp w has the 64 dims of slab w: eight rows x four 16-code words a step
-    // (a staged row is 41 words long, an odd number: eight rows of one word
-    // column lie in eight different bank groups), and one rotary word a thread.
-    const int w = warp - 8, ct = threadIdx.x - 256;
-    int raw = 0;
-    for (int t = 0;; ++t) {
+  } else if (!FP8) {
+    // ------------------------------------------------------------ rows behind the end (bf16)
+    // Every stage passes through this warp, with something to clear or not, and
+    // is freed by it too: a wait for a stage some phases ahead, or behind, would
+    // take another phase of the same parity for its own.
+    int n = 0, nclear = 0;
+    auto landed = [&]() { return wait(&full[n % kStages], (n / kStages) & 1); };
+    for (int t = 0;; ++t, ++n) {
       TileInfo x;
-      bool ok = get_info(t, x);
-      if (!ok || (x.flags & kEnd)) break;
-      const int rs = t % C::kRopes, hc = 2 * t + (w >> 2), hs = hc % C::kHalves;
-      ok = wait(&rope_free[rs], ((t / C::kRopes) & 1) ^ 1) &&
-           wait(&half_free[hs], ((hc / C::kHalves) & 1) ^ 1);
-      const uint32_t slab = smem_u32(halves + hs * kHalf + (w & 3) * kSlab);
-      const uint32_t rope = smem_u32(ropes + rs * kSlab);
-      for (int c = 0; c < 2 && ok; ++c, ++raw) {
-        const int ws = raw % C::kRaws;
-        ok = wait(&raw_full[ws], (raw / C::kRaws) & 1);
-        if (!ok) break;
-        const uint8_t* src = raws + ws * kRawBytes;
-        const uint32_t mask = x.mask[c];
+      if (!get_info(t, x) || (x.flags & kEnd)) break;
+      if (x.flags & kFirst) {
+        if (!landed()) break;
+        warp_arrive(&freed[n % kStages]);
+        ++n;
+      }
+      if (!landed()) break;
+      const int st = n % kStages;
+      if (x.flags & kClear) {
+        const uint32_t base = smem_u32(smem) + st * kTile + (lane >> 3) * kSlab + (lane & 7) * 16;
+#pragma unroll 1
+        for (int r = 0; r < kT; ++r)
+          if (!((x.mask[r >> 5] >> (r & 31)) & 1u)) {
+            st_shared_v4(base + r * 128, make_uint4(0, 0, 0, 0));
+            st_shared_v4(base + 4 * kSlab + r * 128, make_uint4(0, 0, 0, 0));
+          }
+        fence_proxy_async_smem();
+        warp_arrive(&cleared[nclear % kClears]);
+        ++nclear;
+      }
+      warp_arrive(&freed[st]);
+    }
+  } else {
+    // ------------------------------------------------------------ widening (e4m3)
+    // Warp w has the 64 dims of slab w, eight rows x four 16-code words a step
+    // (consecutive lanes have consecutive words of a row; even rows' words go to
+    // even chunks of the swizzle, odd rows' to odd ones, so eight lanes meet
+    // eight chunks), and eight rows of the rotary slab. The tile is taken in two
+    // halves of 32 rows: while one half is widened the other's loads are in
+    // flight, and a half is waited for as a whole before the next is asked for
+    // (loads asked for in between would have to arrive too: a warp has few
+    // scoreboards).
+    const int w = warp - 8;
+    const int wrow = lane >> 2, wch = lane & 3;
+    uint4 code[2][4], rot[2];
+    float scale[2];   // lane l: of row l, and of row 32 + l
+    TileInfo x;
+    const uint8_t* base[4] = {nullptr, nullptr, nullptr, nullptr};  // dense: first row of each 16 of the next tile
+    int ring = 0;  // sparse: descriptor slot of the next tile
+    // row 16 g + r of the next tile, r < 16; g is known to the compiler, or two pointers are
+    auto row_of = [&](const uint8_t* group, int g, int r) -> const uint8_t* {
+      if constexpr (SPARSE) return a.cache + places[ring * kT + 16 * g + r];
+      else return group + r * kLatentRowFp8;
+    };
+    // the next tile's descriptor; its rows' places stay readable until `release`
+    auto fetch = [&](int t) {
+      if (!wait(&info_full[t % kInfo], (t / kInfo) & 1)) return false;
+      x = infos[t % kInfo];
+      ring = t % kInfo;
+      if (!SPARSE)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) base[g] = a.cache + x.at[g];
+      return true;
+    };
+    auto release = [&](int t) { warp_arrive(&info_free[t % kInfo]); };
+    auto load = [&](auto half_c) {  // half `h` of the next tile
+      constexpr int h = decltype(half_c)::value;
+      const uint32_t m = x.mask[h];
+      const bool high = (lane & 16) != 0, rhigh = (w & 4) != 0;
+      const int ri = w * 4 + (lane >> 3);  // rotary: 4 rows x 8 words a half
+      const uint8_t* sp = row_of(high ? base[2 * h + 1] : base[2 * h], 2 * h + high, lane & 15) + 512 + (w >> 1) * 4;
+      const uint8_t* rp = row_of(rhigh ? base[2 * h + 1] : base[2 * h], 2 * h + rhigh, ri & 15) + 528 + (lane & 7) * 16;
+      if (m == 0xffffffffu) {
+        scale[h] = ld_nc_f(sp);
+        rot[h] = ld_nc_v4(rp);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          code[h][j] = ld_nc_v4(row_of(base[2 * h + (j >> 1)], 2 * h + (j >> 1), wrow + (j & 1) * 8) + w * 64 + wch * 16);
+      } else {
+        scale[h] = 1.f;
+        rot[h] = make_uint4(0, 0, 0, 0);
+        if ((m >> lane) & 1u) scale[h] = ld_nc_f(sp);
+        if ((m >> ri) & 1u) rot[h] = ld_nc_v4(rp);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int rr = (lane & 7) + 8 * j, ch = lane >> 3;
-          const uint8_t* rowp = src + rr * kLatentRowFp8;
-          uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          if ((mask >> rr) & 1u)
-            e4m3x16_to_bf16x16(*reinterpret_cast<const uint4*>(rowp + w * 64 + ch * 16),
-                               *reinterpret_cast<const float*>(rowp + 512 + (w >> 1) * 4), o);
-          const int row = c * 32 + rr;
-          st_shared_v4(slab + sw128_offset(row, 2 * ch), make_uint4(o[0], o[1], o[2], o[3]));
-          st_shared_v4(slab + sw128_offset(row, 2 * ch + 1), make_uint4(o[4], o[5], o[6], o[7]));
+          code[h][j] = make_uint4(0, 0, 0, 0);
+          if ((m >> (8 * j + wrow)) & 1u)
+            code[h][j] = ld_nc_v4(row_of(base[2 * h + (j >> 1)], 2 * h + (j >> 1), wrow + (j & 1) * 8) + w * 64 + wch * 16);
         }
-        {
-          const int rr = ct >> 3, ch = ct & 7;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if ((mask >> rr) & 1u) v = *reinterpret_cast<const uint4*>(src + rr * kLatentRowFp8 + 528 + ch * 16);
-          st_shared_v4(rope + sw128_offset(c * 32 + rr, ch), v);
-        }
-        mbar_arrive(&raw_free[ws]);
       }
-      if (!ok) break;
-      fence_proxy_async_smem();
-      mbar_arrive(&rope_full[rs]);
-      mbar_arrive(&half_full[hs]);
+    };
+    auto arrived = [&](auto half_c) {
+      constexpr int h = decltype(half_c)::value;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) use_now(code[h][j]);
+      use_now(rot[h]);
+      asm volatile("" : "+f"(scale[h])::"memory");
+    };
+    auto widen = [&](auto half_c, uint32_t tile) {
+      constexpr int h = decltype(half_c)::value;
+      st_shared_v4(tile + 8 * kSlab + h * 4096 + sw128_offset(w * 4 + (lane >> 3), lane & 7), rot[h]);
+      const uint32_t dst0 = tile + w * kSlab + h * 4096 + sw128_offset(wrow, 2 * wch);
+      const uint32_t dst1 = tile + w * kSlab + h * 4096 + sw128_offset(wrow, 2 * wch + 1);
+      const uint32_t mine = widen_factor(scale[h]);
+      uint32_t rare = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t f = __shfl_sync(0xffffffffu, mine, 8 * j + wrow);
+        rare |= has_nan(code[h][j]) | (f == kNoFactor ? 1u : 0u);
+        uint32_t o[8];
+        widen16(code[h][j], f, o);
+        st_shared_v4(dst0 + j * 1024, make_uint4(o[0], o[1], o[2], o[3]));
+        st_shared_v4(dst1 + j * 1024, make_uint4(o[4], o[5], o[6], o[7]));
+      }
+      if (__any_sync(0xffffffffu, rare != 0)) {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const uint4 c = j == 0 ? code[h][0] : j == 1 ? code[h][1] : j == 2 ? code[h][2] : code[h][3];
+          uint32_t o[8];
+          e4m3x16_to_bf16x16(c, __shfl_sync(0xffffffffu, scale[h], 8 * j + wrow), o);
+          st_shared_v4(dst0 + j * 1024, make_uint4(o[0], o[1], o[2], o[3]));
+          st_shared_v4(dst1 + j * 1024, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+      }
+    };
+    const std::integral_constant<int, 0> half0;
+    const std::integral_constant<int, 1> half1;
+    bool ok = fetch(0);
+    bool more = ok && !(x.flags & kEnd), first = true;
+    int b = x.b, qn = -1;  // stage of the last Q that this warp has copied
+    if (more) {
+      load(half0);
+      load(half1);
     }
+    if (ok) release(0);
+    int n = 0;
+    for (int t = 0; more; ++t, ++n) {
+      if (first) {  // the first of these warps copies Q
+        if (w == 0) {
+          const int qs = n % kStages;
+          ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_n(&full[qs], 7);
+            mbar_arrive_expect_tx(&full[qs], 9 * kQSlab);
+          }
+          __syncwarp();
+          if (lane < 9) copy_q(b, qs, lane);
+          __syncwarp();
+          qn = n;
+        }
+        ++n;
+      }
+      const int st = n % kStages;
+      ok = fetch(t + 1) && wait(&freed[st], ((n / kStages) & 1) ^ 1);
+      if (!ok) break;
+      more = !(x.flags & kEnd);
+      first = (x.flags & kFirst) != 0;
+      b = x.b;
+      const uint32_t tile = smem_u32(smem) + st * kTile;
+      arrived(half0);
+      widen(half0, tile);
+      arrived(half1);
+      if (more) load(half0);
+      widen(half1, tile);
+      fence_proxy_async_smem();
+      warp_arrive(&full[st]);
+      if (more) {
+        arrived(half0);
+        load(half1);
+      }
+      release(t + 1);
+    }
+    // given up: the copy lands before the CTA exits (else the piece's products have waited for it)
+    if (!ok && qn >= 0 && lane == 0) mbar_drain(&full[qn % kStages], (qn / kStages) & 1);
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -805,10 +932,12 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
     if (gf == gl) return;  // one piece: written already
   }
   const bool live = row < a.rows;
-  const int rb = row >> 6, r = row & 63;
+  const int rb = row / kM, r = row % kM;
+  // only the first of the groups may hold another sequence before this one
+  const int first_slot = bt > 0 && gf * total / G < start ? 1 : 0;
   auto part_row = [&](int g) {
-    const int slot = 2 * g + (g * total / G >= start ? 0 : 1);
-    return (static_cast<int64_t>(slot) * a.rblocks + rb) * 64 + r;
+    const int slot = 2 * g + (g == gf ? first_slot : 0);
+    return (static_cast<int64_t>(slot) * a.rblocks + rb) * kM + r;
   };
   const float sink2 = a.sink && live ? a.sink[row % a.H] * kLog2e : -INFINITY;
   float M = sink2, den = 0.f;
@@ -827,7 +956,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     if (sink2 != -INFINITY) den += exp2f(sink2 - M);
-#pragma unroll 4
+#pragma unroll 2
     for (int g = gf + warp % WPR; g <= gl; g += WPR) {
       const int64_t pr = part_row(g);
       const float m = ml[pr].x;
@@ -883,7 +1012,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
 
 template <bool FP8, bool SPARSE>
 cudaError_t launch_main(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, cudaStream_t stream) {
-  using C = Cfg<FP8>;
+  using C = Cfg<FP8, SPARSE>;
   auto kern = latent_attention_kernel<FP8, SPARSE>;
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, done);

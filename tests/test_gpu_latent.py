@@ -316,6 +316,8 @@ DECODE = [
     ([1], 1, 1, 16), ([0], 1, 3, 16), ([63], 1, 64, 16), ([64], 1, 8, 64), ([65, 0, 1], 1, 65, 32),
     ([200, 131, 7, 0, 64], 1, 128, 48), ([300, 2, 1, 0], 4, 5, 16), ([1000, 513], 2, 128, 64),
     ([5000], 1, 16, 128), ([4097, 1], 3, 33, 64), ([130] * 70, 1, 16, 16),
+    # a dozen tiles and more in every share, and shares that pass from one sequence to the next, and over a short one
+    ([61000, 0, 70, 64064], 1, 4, 64), ([9000, 3, 11111], 2, 64, 32), ([640] * 300, 1, 2, 16),
 ]
 
 
@@ -402,7 +404,7 @@ def test_decode_refuses(ops):
             ops.latent_decode(**{**args, **kw})
 
 
-SPARSE = [(1, 1, 1, 16), (2, 8, 63, 16), (3, 128, 64, 64), (1, 65, 257, 32), (4, 16, 2048, 64), (40, 3, 100, 48)]
+SPARSE = [(150, 2, 1000, 64), (1, 1, 1, 16), (2, 8, 63, 16), (3, 128, 64, 64), (1, 65, 257, 32), (4, 16, 2048, 64), (40, 3, 100, 48)]
 
 
 @pytest.mark.parametrize("B,H,k,page", SPARSE)
@@ -541,3 +543,31 @@ def test_captured_graphs_and_side_streams(ops):
     out, lse = ops.latent_decode(q, caches[1], table, lens, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(out, outs[1][0]) and torch.equal(lse, outs[1][1])
+
+
+@pytest.mark.parametrize("page_gap", [0, 16])
+def test_every_code_and_scale_is_widened(ops, page_gap):
+    """Sequences of one row: the output is the row itself, whatever its codes and scales (powers of two near and far,
+    and others). The weight 2^(z - max) is off from 1 by less than 2^-20, and so is the output."""
+    scales = [1.0, 2.0 ** -100, 2.0 ** 7, 2.0 ** 8, 2.0 ** 100, 0.3, 1.5, 2.0 ** -126]
+    n = len(scales)
+    big = ops.new_latent_cache(n, 16 + page_gap, True)
+    cache = big[:, :16]
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda")
+    codes[codes & 0x7f == 0x7f] = 0  # NaN
+    rows = cache[:, 3]
+    rows[:, :512] = codes.repeat(2)
+    rows[:, 512:528] = torch.tensor(scales, device="cuda")[:, None].repeat(1, 4).view(torch.uint8)
+    want = f64(torch.from_numpy(L.unpack(rows).astype(np.float32)).to(torch.bfloat16))[:, :512]
+    q = torch.zeros(n, 5, 576, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(n, device="cuda", dtype=torch.int32)[:, None] * 16 + 3
+    first = cache.clone()
+    first[:, 0] = rows
+    table = torch.arange(n, device="cuda", dtype=torch.int32)[:, None]
+    for out in (ops.latent_sparse_decode(q, cache, slots, out_dtype=torch.float32)[0],
+                ops.latent_decode(q, first, table, torch.ones(n, dtype=torch.int64, device="cuda"), out_dtype=torch.float32)[0]):
+        assert np.all(np.abs(f64(out) - want[:, None]) <= np.abs(want[:, None]) * 2.0 ** -18 + 2.0 ** -140)
+    rows[0, 77] = 0x7f
+    rows[1, 78] = 0xff
+    out = ops.latent_sparse_decode(q, cache, slots)[0]
+    assert out[:2].isnan().all() and not out[2:].isnan().any()
