@@ -487,36 +487,7 @@ IC_DEV void e4m3x16_to_bf16x16(const uint4& c, float scale, uint32_t (&o)[8]) {
   }
 }
 
-// The same by bits, for a scale that is a power of two. Code bits seeeemmm
-// moved to s0000eeeemmm0000 are a bf16 of 2^-120 times the code's value,
-// subnormal codes included, so one multiplication by 2^120 scale finishes two
-// codes. widen_factor gives that factor twice, or kNoFactor where the scale is
-// no power of two or leaves bf16's range with 2^120; has_nan is nonzero where
-// one of the codes is 0x7f or 0xff (NaN, which the bits do not show): both then
-// need e4m3x16_to_bf16x16.
-constexpr uint32_t kNoFactor = 0xffffffffu;
-IC_DEV uint32_t widen_factor(float scale) {
-  const uint32_t sb = __float_as_uint(scale), e = sb >> 23;
-  return (sb & 0x7fffffu) == 0 && e >= 1 && e <= 134 ? (e + 120) * 0x00800080u : kNoFactor;
-}
-IC_DEV uint32_t has_nan(const uint4& c) {
-  return (((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
-          ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
-}
-IC_DEV void widen16(const uint4& c, uint32_t factor, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  const __nv_bfloat162 mul = *reinterpret_cast<const __nv_bfloat162*>(&factor);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t hi = (w[i] & 0x80808080u) | ((w[i] >> 4) & 0x07070707u), lo = (w[i] << 4) & 0xf0f0f0f0u;
-    const uint32_t u0 = __byte_perm(lo, hi, 0x5140), u1 = __byte_perm(lo, hi, 0x7362);
-    const __nv_bfloat162 p0 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u0), mul);
-    const __nv_bfloat162 p1 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u1), mul);
-    o[2 * i] = *reinterpret_cast<const uint32_t*>(&p0);
-    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&p1);
-  }
-}
-// The last code of `w` is read before anything that follows is issued.
+// What was loaded into w is waited for before anything that follows is issued.
 IC_DEV void use_now(uint4& w) { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)::"memory"); }
 
 // 16 bytes that no thread of the kernel writes, past L1.

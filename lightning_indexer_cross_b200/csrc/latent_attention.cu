@@ -40,9 +40,9 @@
 // there; warps 4-7 load Q and run the softmax and the output. bf16 pages: warp
 // 3 issues TMA boxes that land in the operand layout, warp 8 clears the rows
 // behind a sequence's end (a zero weight times a NaN left there would be NaN).
-// e4m3 pages: warps 8-15 hold the next tile's codes in registers, straight from
-// L2, and widen them into the operand layout (staging them in shared memory
-// would add 84 KB to its traffic).
+// e4m3 pages: warps 8-15 take a tile's codes to registers, straight from L2, and
+// widen them into the operand layout (staging them in shared memory would add
+// 84 KB to its traffic).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -181,10 +181,13 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  // one thread's wait, and a whole warp's: its lanes leave a wait that was
-  // given up together, so that no lane stays behind in a warp-wide instruction
-  auto wait1 = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_hot(bar, parity, abort_flag, a.status, a.wait_ns); };
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait1(bar, parity)) != 0; };
+  // A whole warp waits: its lanes leave a wait that was given up together, so
+  // that no lane stays behind in a warp-wide instruction. (A lane that waits
+  // alone wakes late: 430 to 690 cycles after the arrival against 120 to 140,
+  // measured with 2 to 24 waiting warps.)
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_hot(bar, parity, abort_flag, a.status, a.wait_ns)) != 0;
+  };
   // one arrival for the warp, after all its lanes' writes. (The lanes meet
   // again before any of them can enter a wait: a try suspends the warp, and the
   // one lane's work would wait with it.)
@@ -193,13 +196,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     if (lane == 0) mbar_arrive(bar);
     __syncwarp();
   };
-  // the descriptor of tile t, read by one thread or by a whole warp
-  auto get_info1 = [&](int t, TileInfo& x) {
-    if (!wait1(&info_full[t % kInfo], (t / kInfo) & 1)) return false;
-    x = infos[t % kInfo];
-    mbar_arrive(&info_free[t % kInfo]);
-    return true;
-  };
+  // the descriptor of tile t
   auto get_info = [&](int t, TileInfo& x) {
     if (!wait(&info_full[t % kInfo], (t / kInfo) & 1)) return false;
     x = infos[t % kInfo];
@@ -366,24 +363,26 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q . K^T
-    if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kM, kT, false, false);
-      const uint32_t ka = smem_u32(smem);
-      int pieces = 0, n = 0;  // stages used so far
-      for (int t = 0;; ++t, ++n) {
-        TileInfo x;
-        if (!get_info1(t, x) || (x.flags & kEnd)) break;
-        if (x.flags & kFirst) {
-          if (!wait1(q_full, pieces & 1)) break;
-          mbar_arrive(&freed[n % kStages]);
-          ++pieces;
-          ++n;
-        }
-        // the logits of tile t - 2 have been read
-        if (t >= 2 && !wait1(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
-        const int st = n % kStages;
-        if (!wait1(&full[st], (n / kStages) & 1)) break;
-        tc_fence_after();
+    constexpr uint32_t idesc = idesc_bf16_f32(kM, kT, false, false);
+    const uint32_t ka = smem_u32(smem);
+    int pieces = 0, n = 0;  // stages used so far
+#pragma unroll 1
+    for (int t = 0;; ++t, ++n) {
+      TileInfo x;
+      if (!get_info(t, x) || (x.flags & kEnd)) break;
+      if (x.flags & kFirst) {
+        if (!wait(q_full, pieces & 1)) break;
+        if (lane == 0) mbar_arrive(&freed[n % kStages]);
+        __syncwarp();
+        ++pieces;
+        ++n;
+      }
+      // the logits of tile t - 2 have been read
+      if (t >= 2 && !wait(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
+      const int st = n % kStages;
+      if (!wait(&full[st], (n / kStages) & 1)) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint32_t d = tmem + kSCol + (t & 1) * 16;
         const uint64_t bd = sw128_desc(ka + st * kTile, 16, 1024);
 #pragma unroll 1
@@ -394,34 +393,37 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
         mma_commit(&s_full[t & 1]);
         if (x.flags & kLast) mma_commit(q_free);
       }
-      // every MMA issued has retired before TMEM is released
-      mma_commit(retire);
-      mbar_drain(retire, 0);
+      __syncwarp();
     }
+    // every MMA issued has retired before TMEM is released (the lane that
+    // elect_one names is the same each time)
+    if (elect_one()) mma_commit(retire);
     __syncwarp();
+    mbar_drain(retire, 0);
   } else if (warp == 2) {
     // ------------------------------------------------------------ O += P . V
-    if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kM, 256, false, true);
-      const uint32_t va = smem_u32(smem), pa = smem_u32(ps);
-      int pieces = 0, nclear = 0, n = 0;
-      for (int t = 0;; ++t, ++n) {
-        TileInfo x;
-        if (!get_info1(t, x) || (x.flags & kEnd)) break;
-        const bool first = (x.flags & kFirst) != 0;
-        if (first) {
-          if (pieces > 0 && !wait1(o_free, (pieces - 1) & 1)) break;
-          ++pieces;
-          ++n;
-        }
-        if (!FP8 && (x.flags & kClear)) {
-          if (!wait1(&cleared[nclear % kClears], (nclear / kClears) & 1)) break;
-          ++nclear;
-        }
-        const int st = n % kStages;
-        if (!wait1(&full[st], (n / kStages) & 1)) break;
-        if (!wait1(&p_ready[t & 1], (t >> 1) & 1)) break;
-        tc_fence_after();
+    constexpr uint32_t idesc = idesc_bf16_f32(kM, 256, false, true);
+    const uint32_t va = smem_u32(smem), pa = smem_u32(ps);
+    int pieces = 0, nclear = 0, n = 0;
+#pragma unroll 1
+    for (int t = 0;; ++t, ++n) {
+      TileInfo x;
+      if (!get_info(t, x) || (x.flags & kEnd)) break;
+      const bool first = (x.flags & kFirst) != 0;
+      if (first) {
+        if (pieces > 0 && !wait(o_free, (pieces - 1) & 1)) break;
+        ++pieces;
+        ++n;
+      }
+      if (!FP8 && (x.flags & kClear)) {
+        if (!wait(&cleared[nclear % kClears], (nclear / kClears) & 1)) break;
+        ++nclear;
+      }
+      const int st = n % kStages;
+      if (!wait(&full[st], (n / kStages) & 1)) break;
+      if (!wait(&p_ready[t & 1], (t >> 1) & 1)) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint64_t vd = sw128_desc(va + st * kTile, kSlab, 1024), pd = sw128_desc(pa + (t & 1) * kP, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
@@ -432,10 +434,11 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
         mma_commit(&freed[st]);
         mma_commit(&pv_done[t & 1]);
       }
-      mma_commit(retire);
-      mbar_drain(retire, 0);
+      __syncwarp();
     }
+    if (elect_one()) mma_commit(retire);
     __syncwarp();
+    mbar_drain(retire, 0);
   } else if (warp == 3) {
     // ------------------------------------------------------------ copies (bf16)
     // The stages have one producer that fills them in order: a second one that
@@ -567,28 +570,31 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
         }
         sum = (part[0] + part[1]) + (part[2] + part[3]);
       };
-      // weights under the old reference, while the other quarters' maxima
-      // come: most tiles leave it where it is
-      const bool early = __any_sync(0xffffffffu, ref != -INFINITY) != 0;
-      if (early) weigh(ref == -INFINITY ? 0.f : ref);
-      float other[4];
-      ok = take(other);
-      if (!ok) break;
-      const float m = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3])) * c2;
-      // the reference moves when the row's maximum passes it by more than
-      // kMove: weights stay below 2^8, far from bf16's and fp32's limits
+      // First under the old reference, while the other quarters' maxima come
+      // (most tiles leave it where it is), and again if it has moved. (A row
+      // with nothing valid so far: every weight is 0.)
       float scale = 1.f;
-      bool moved = false;
-      if (ref == -INFINITY) {
-        moved = m != -INFINITY;
-        ref = m;
-      } else if (m > ref + kMove) {
-        scale = ex2_approx(ref - m);
-        ref = m;
-        moved = true;
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        weigh(ref == -INFINITY ? 0.f : ref);
+        if (pass) break;
+        float other[4];
+        ok = take(other);
+        const float m = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3])) * c2;
+        // the reference moves when the row's maximum passes it by more than
+        // kMove: weights stay below 2^8, far from bf16's and fp32's limits
+        bool moved = false;
+        if (ref == -INFINITY) {
+          moved = m != -INFINITY;
+          ref = m;
+        } else if (m > ref + kMove) {
+          scale = ex2_approx(ref - m);
+          ref = m;
+          moved = true;
+        }
+        if (!__any_sync(0xffffffffu, moved)) break;
       }
-      // (a row with nothing valid so far: every weight is 0)
-      if (!early || __any_sync(0xffffffffu, moved)) weigh(ref == -INFINITY ? 0.f : ref);
+      if (!ok) break;
       l = fmaf(l, scale, sum);
       // the product of two tiles ago has read its weights
       if (t >= 2) ok = wait(&pv_done[t & 1], ((t >> 1) - 1) & 1);
@@ -727,144 +733,116 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ widening (e4m3)
-    // Warp w has the 64 dims of slab w, eight rows x four 16-code words a step
-    // (consecutive lanes have consecutive words of a row; even rows' words go to
-    // even chunks of the swizzle, odd rows' to odd ones, so eight lanes meet
-    // eight chunks), and eight rows of the rotary slab. The tile is taken in two
-    // halves of 32 rows: while one half is widened the other's loads are in
-    // flight, and a half is waited for as a whole before the next is asked for
-    // (loads asked for in between would have to arrive too: a warp has few
-    // scoreboards).
+    // Warp w has eight rows of the tile, in two units of four. A load takes a
+    // whole row's codes, lane l the 16 of word l: four lines an instruction
+    // (64-byte pieces of eight rows cost four times the lookups in L1, which then
+    // bound the kernel). Eight lanes that store together have four words of two
+    // neighbouring slabs; those of the odd slab store their second half first, so
+    // the eight meet eight chunks of the swizzle. The next unit's loads are in
+    // flight while one is widened.
     const int w = warp - 8;
-    const int wrow = lane >> 2, wch = lane & 3;
-    uint4 code[2][4], rot[2];
-    float scale[2];   // lane l: of row l, and of row 32 + l
+    struct Unit {
+      uint4 code[4], rot;  // rot: word lane & 7 of row lane >> 3
+      float scale;         // lane l < 16: group l & 3 of row l >> 2
+    } cur, nxt;
+    const int odd = (lane >> 2) & 1, wch = lane & 3;
     TileInfo x;
-    const uint8_t* base[4] = {nullptr, nullptr, nullptr, nullptr};  // dense: first row of each 16 of the next tile
-    int ring = 0;  // sparse: descriptor slot of the next tile
-    // row 16 g + r of the next tile, r < 16; g is known to the compiler, or two pointers are
-    auto row_of = [&](const uint8_t* group, int g, int r) -> const uint8_t* {
-      if constexpr (SPARSE) return a.cache + places[ring * kT + 16 * g + r];
-      else return group + r * kLatentRowFp8;
-    };
-    // the next tile's descriptor; its rows' places stay readable until `release`
+    int ring = 0;  // descriptor slot of x
     auto fetch = [&](int t) {
-      if (!wait(&info_full[t % kInfo], (t / kInfo) & 1)) return false;
-      x = infos[t % kInfo];
       ring = t % kInfo;
-      if (!SPARSE)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) base[g] = a.cache + x.at[g];
+      if (!wait(&info_full[ring], (t / kInfo) & 1)) return false;
+      x = infos[ring];
       return true;
     };
-    auto release = [&](int t) { warp_arrive(&info_free[t % kInfo]); };
-    auto load = [&](auto half_c) {  // half `h` of the next tile
-      constexpr int h = decltype(half_c)::value;
-      const uint32_t m = x.mask[h];
-      const bool high = (lane & 16) != 0, rhigh = (w & 4) != 0;
-      const int ri = w * 4 + (lane >> 3);  // rotary: 4 rows x 8 words a half
-      const uint8_t* sp = row_of(high ? base[2 * h + 1] : base[2 * h], 2 * h + high, lane & 15) + 512 + (w >> 1) * 4;
-      const uint8_t* rp = row_of(rhigh ? base[2 * h + 1] : base[2 * h], 2 * h + rhigh, ri & 15) + 528 + (lane & 7) * 16;
-      if (m == 0xffffffffu) {
-        scale[h] = ld_nc_f(sp);
-        rot[h] = ld_nc_v4(rp);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          code[h][j] = ld_nc_v4(row_of(base[2 * h + (j >> 1)], 2 * h + (j >> 1), wrow + (j & 1) * 8) + w * 64 + wch * 16);
-      } else {
-        scale[h] = 1.f;
-        rot[h] = make_uint4(0, 0, 0, 0);
-        if ((m >> lane) & 1u) scale[h] = ld_nc_f(sp);
-        if ((m >> ri) & 1u) rot[h] = ld_nc_v4(rp);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          code[h][j] = make_uint4(0, 0, 0, 0);
-          if ((m >> (8 * j + wrow)) & 1u)
-            code[h][j] = ld_nc_v4(row_of(base[2 * h + (j >> 1)], 2 * h + (j >> 1), wrow + (j & 1) * 8) + w * 64 + wch * 16);
-        }
-      }
-    };
-    auto arrived = [&](auto half_c) {
-      constexpr int h = decltype(half_c)::value;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) use_now(code[h][j]);
-      use_now(rot[h]);
-      asm volatile("" : "+f"(scale[h])::"memory");
-    };
-    auto widen = [&](auto half_c, uint32_t tile) {
-      constexpr int h = decltype(half_c)::value;
-      st_shared_v4(tile + 8 * kSlab + h * 4096 + sw128_offset(w * 4 + (lane >> 3), lane & 7), rot[h]);
-      const uint32_t dst0 = tile + w * kSlab + h * 4096 + sw128_offset(wrow, 2 * wch);
-      const uint32_t dst1 = tile + w * kSlab + h * 4096 + sw128_offset(wrow, 2 * wch + 1);
-      const uint32_t mine = widen_factor(scale[h]);
-      uint32_t rare = 0;
+    auto load = [&](int h) {  // rows 8 w + 4 h + [0, 4) of x's tile
+      const int r0 = 8 * w + 4 * h;
+      const uint32_t m = (w & 4 ? x.mask[1] : x.mask[0]) >> (r0 & 31);
+      const uint8_t* base = a.cache;  // dense: the first of the four rows
+      if constexpr (!SPARSE)
+        base += (w & 4 ? (w & 2 ? x.at[3] : x.at[2]) : (w & 2 ? x.at[1] : x.at[0])) + (r0 & 15) * kLatentRowFp8;
+      auto row_of = [&](int j) -> const uint8_t* {
+        if constexpr (SPARSE) return a.cache + places[ring * kT + r0 + j];
+        else return base + j * kLatentRowFp8;
+      };
+      nxt.scale = 1.f;
+      nxt.rot = make_uint4(0, 0, 0, 0);
+      if (lane < 16 && ((m >> (lane >> 2)) & 1u)) nxt.scale = ld_nc_f(row_of(lane >> 2) + 512 + (lane & 3) * 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t f = __shfl_sync(0xffffffffu, mine, 8 * j + wrow);
-        rare |= has_nan(code[h][j]) | (f == kNoFactor ? 1u : 0u);
-        uint32_t o[8];
-        widen16(code[h][j], f, o);
-        st_shared_v4(dst0 + j * 1024, make_uint4(o[0], o[1], o[2], o[3]));
-        st_shared_v4(dst1 + j * 1024, make_uint4(o[4], o[5], o[6], o[7]));
+        nxt.code[j] = make_uint4(0, 0, 0, 0);
+        if ((m >> j) & 1u) nxt.code[j] = ld_nc_v4(row_of(j) + lane * 16);
       }
-      if (__any_sync(0xffffffffu, rare != 0)) {
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          const uint4 c = j == 0 ? code[h][0] : j == 1 ? code[h][1] : j == 2 ? code[h][2] : code[h][3];
-          uint32_t o[8];
-          e4m3x16_to_bf16x16(c, __shfl_sync(0xffffffffu, scale[h], 8 * j + wrow), o);
-          st_shared_v4(dst0 + j * 1024, make_uint4(o[0], o[1], o[2], o[3]));
-          st_shared_v4(dst1 + j * 1024, make_uint4(o[4], o[5], o[6], o[7]));
-        }
-      }
+      if ((m >> (lane >> 3)) & 1u) nxt.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
     };
-    const std::integral_constant<int, 0> half0;
-    const std::integral_constant<int, 1> half1;
     bool ok = fetch(0);
-    bool more = ok && !(x.flags & kEnd), first = true;
-    int b = x.b, qn = -1;  // stage of the last Q that this warp has copied
-    if (more) {
-      load(half0);
-      load(half1);
-    }
-    if (ok) release(0);
-    int n = 0;
-    for (int t = 0; more; ++t, ++n) {
-      if (first) {  // the first of these warps copies Q
-        if (w == 0) {
-          const int qs = n % kStages;
-          ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_n(&full[qs], 7);
-            mbar_arrive_expect_tx(&full[qs], 9 * kQSlab);
+    bool more = ok && !(x.flags & kEnd);
+    if (more) load(0);
+    int n = 0, b = x.b, qn = -1;  // qn: stage of the last Q that this warp has copied
+    bool first = true;
+    uint32_t tile = 0;
+#pragma unroll 1
+    for (int u = 0; more; ++u) {
+      const int t = u >> 1, h = u & 1;
+      if (h == 0) {
+        if (first) {  // the first of these warps copies Q
+          if (w == 0) {
+            const int qs = n % kStages;
+            ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_n(&full[qs], 7);
+              mbar_arrive_expect_tx(&full[qs], 9 * kQSlab);
+            }
+            __syncwarp();
+            if (lane < 9) copy_q(b, qs, lane);
+            __syncwarp();
+            qn = n;
           }
-          __syncwarp();
-          if (lane < 9) copy_q(b, qs, lane);
-          __syncwarp();
-          qn = n;
+          ++n;
         }
+        tile = smem_u32(smem) + (n % kStages) * kTile;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) use_now(nxt.code[j]);  // the unit has arrived
+      use_now(nxt.rot);
+      cur = nxt;
+      if (h == 0) {
+        load(1);
+        warp_arrive(&info_free[ring]);
+      } else {
+        ok = fetch(t + 1);
+        if (!ok) break;
+        more = !(x.flags & kEnd);
+        first = (x.flags & kFirst) != 0;
+        b = x.b;
+        if (more) load(0);
+      }
+      // all four rows at once, with nothing ordered in between: two warps a
+      // scheduler leave it to one warp's independent instructions to fill it
+      uint32_t o[4][8];
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = __shfl_sync(0xffffffffu, cur.scale, 4 * j + (lane >> 3));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e4m3x16_to_bf16x16(cur.code[j], f[j], o[j]);
+      if (h == 0) {
+        ok = wait(&freed[n % kStages], ((n / kStages) & 1) ^ 1);
+        if (!ok) break;
+      }
+      const int r0 = 8 * w + 4 * h;
+      st_shared_v4(tile + 8 * kSlab + sw128_offset(r0 + (lane >> 3), lane & 7), cur.rot);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 lo = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]), hi = make_uint4(o[j][4], o[j][5], o[j][6], o[j][7]);
+        const uint32_t dst = tile + (lane >> 2) * kSlab;
+        st_shared_v4(dst + sw128_offset(r0 + j, 2 * wch + odd), odd ? hi : lo);
+        st_shared_v4(dst + sw128_offset(r0 + j, 2 * wch + 1 - odd), odd ? lo : hi);
+      }
+      if (h == 1) {
+        fence_proxy_async_smem();
+        warp_arrive(&full[n % kStages]);
         ++n;
       }
-      const int st = n % kStages;
-      ok = fetch(t + 1) && wait(&freed[st], ((n / kStages) & 1) ^ 1);
-      if (!ok) break;
-      more = !(x.flags & kEnd);
-      first = (x.flags & kFirst) != 0;
-      b = x.b;
-      const uint32_t tile = smem_u32(smem) + st * kTile;
-      arrived(half0);
-      widen(half0, tile);
-      arrived(half1);
-      if (more) load(half0);
-      widen(half1, tile);
-      fence_proxy_async_smem();
-      warp_arrive(&full[st]);
-      if (more) {
-        arrived(half0);
-        load(half1);
-      }
-      release(t + 1);
     }
     // given up: the copy lands before the CTA exits (else the piece's products have waited for it)
     if (!ok && qn >= 0 && lane == 0) mbar_drain(&full[qn % kStages], (qn / kStages) & 1);
