@@ -419,7 +419,7 @@ bool paged_cache_ok(const void* cache, ic_dtype_t dtype, int64_t num_pages, int 
   return page_stride >= row * page_size && page_stride % 16 == 0;
 }
 
-// Shares of the tiles: one CTA per SM for the blocks of 32 query rows of each
+// Shares of the tiles: one CTA per SM for the blocks of query rows of each
 // share, but no more shares than two-tile pieces of the longest contexts.
 int latent_groups(int64_t max_tiles, int rblocks) {
   const int64_t g = std::max(1, num_sms() / rblocks);
@@ -433,9 +433,9 @@ struct LatentLayout {
 
 LatentLayout latent_layout(int64_t B, int64_t rows, int64_t max_len) {
   LatentLayout L{};
-  L.rblocks = static_cast<int>(ceil_div<int64_t>(rows, ic::kLatentRows));
+  L.rblocks = static_cast<int>(ceil_div<int64_t>(rows, ic::latent_block(rows)));
   L.groups = latent_groups(B * ceil_div<int64_t>(max_len, ic::kLatentTile), L.rblocks);
-  const size_t pieces = size_t(2) * L.groups * L.rblocks * ic::kLatentRows;
+  const size_t pieces = size_t(2) * L.groups * L.rblocks * ic::latent_block(rows);
   L.o_off = kStatusBytes;
   L.ml_off = align256(L.o_off + pieces * 512 * 4);
   L.total = align256(L.ml_off + pieces * 2 * 4);
@@ -458,7 +458,7 @@ ic_status_t latent_impl(const void* q, const void* cache, ic_dtype_t dtype, int6
   const int64_t max_len = sparse ? k : static_cast<int64_t>(table_width) * page_size;
   if (max_len >= (int64_t(1) << 31) - 64) return IC_ERR_INVALID_ARG;
   // one CTA row block (or one joining CTA) each, and q's rows, in 31 bits
-  if (rows * B >= (int64_t(1) << 31) - 64) return IC_ERR_INVALID_ARG;
+  if (ceil_div<int64_t>(rows, 32) * B * 32 >= (int64_t(1) << 31) - 64) return IC_ERR_INVALID_ARG;
   const LatentLayout L = latent_layout(B, rows, max_len);
   if (ws_bytes < L.total) return IC_ERR_INVALID_ARG;
   EncodeTiledFn enc = encode_fn();
@@ -468,7 +468,7 @@ ic_status_t latent_impl(const void* q, const void* cache, ic_dtype_t dtype, int6
   {
     const cuuint64_t dims[2] = {576, static_cast<cuuint64_t>(rows * B)};
     const cuuint64_t strides[1] = {576 * 2};
-    const cuuint32_t box[2] = {64, ic::kLatentRows};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(ic::latent_block(rows))};
     if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -501,6 +501,7 @@ ic_status_t latent_impl(const void* q, const void* cache, ic_dtype_t dtype, int6
   a.Q = Q;
   a.H = H;
   a.rows = static_cast<int>(rows);
+  a.block = ic::latent_block(rows);
   a.rblocks = L.rblocks;
   a.groups = L.groups;
   a.sink = sink;

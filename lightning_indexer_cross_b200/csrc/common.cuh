@@ -358,6 +358,12 @@ IC_DEV void tmem_ld_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// The two by the array's size.
+IC_DEV void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_issue(taddr, r); }
+IC_DEV void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32_issue(taddr, r); }
+IC_DEV void tmem_ld_wait_for(uint32_t (&r)[16]) { tmem_ld_wait16(r); }
+IC_DEV void tmem_ld_wait_for(uint32_t (&r)[32]) { tmem_ld_wait(r); }
+
 // 32 columns of registers to TMEM; tmem_st_wait before another thread or an
 // MMA uses them.
 IC_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {

@@ -265,7 +265,8 @@ cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t s
 
 // ---------------------------------------------------------------- attention over the paged latent cache
 constexpr int kLatentTile = 64;  // keys of a tile
-constexpr int kLatentRows = 32;  // query rows of a block
+// Query rows of a CTA.
+inline int latent_block(int64_t rows) { return rows <= 32 ? 32 : 64; }
 
 struct LatentArgs {
   const uint8_t* cache;
@@ -279,7 +280,8 @@ struct LatentArgs {
   int k;
   int B, Q, H;
   int rows;              // Q * H query rows of a sequence
-  int rblocks;           // ceil(rows / kLatentRows)
+  int block;             // query rows of a CTA (latent_block)
+  int rblocks;           // ceil(rows / block)
   int groups;            // shares of the tiles; groups * rblocks CTAs
   const float* sink;     // [H] or null
   const __nv_bfloat16* gate;  // [B, Q, H, 512] or null
@@ -287,14 +289,14 @@ struct LatentArgs {
   void* out;             // [B, Q, H, 512]
   int out_f32;
   float* lse;            // [B, Q, H] or null
-  float* part_o;         // [2 groups][rblocks][kLatentRows][512]
-  float* part_ml;        // [2 groups][rblocks][kLatentRows][2]
+  float* part_o;         // [2 groups][rblocks][512 / 4][block][4]
+  float* part_ml;        // [2 groups][rblocks][block][2]
   int* status;
   uint64_t wait_ns;
 };
 // kvmap (bf16 pages): 3-D map (576, page_size, num_pages), box 64 x box_rows x 1,
 // 128-byte swizzle; e4m3 pages are copied without a map (any valid map).
-// qmap: 2-D map over q as [B * rows, 576] bf16, box 64 x kLatentRows, 128-byte swizzle.
+// qmap: 2-D map over q as [B * rows, 576] bf16, box 64 x block, 128-byte swizzle.
 cudaError_t launch_latent_attention(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, bool fp8,
                                     bool sparse, cudaStream_t stream, int* launches);
 

@@ -57,12 +57,6 @@ namespace {
 constexpr int kT = kLatentTile;
 constexpr int kSlab = kT * 128;       // 64 rows x 64 dims, bf16
 constexpr int kTile = 9 * kSlab;      // 64 rows of 576 dims: slabs 0-7 latent, 8 rotary
-constexpr int kStages = 3;            // tiles in shared memory
-constexpr int kClears = kStages + 1;  // as many tiles with cleared rows may be waiting for their product, and one more
-constexpr int kM = kLatentRows;       // query rows of a CTA
-constexpr int kP = kM * 128;          // 32 rows x 64 weights, bf16
-constexpr int kQSlab = kM * 128;      // 32 rows x 64 dims of Q, bf16
-constexpr uint32_t kOutCol = 0, kSCol = 128, kQCol = 160;  // TMEM columns: 128 of O, 2 x 16 of S, 288 of Q
 constexpr int kMinTiles = 2;          // tiles of a group, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.f;          // log2 units by which a row's maximum may pass its reference
@@ -76,20 +70,39 @@ struct TileInfo {
   int64_t at[4];     // dense: byte offset of each 16 rows (e4m3), or page of each box (bf16; -1: none)
 };
 
-template <bool FP8, bool SPARSE>
+// M query rows a CTA. Thread (quadrant, lane) of the softmax has query row
+// `row` of the block and part `part` of the columns.
+template <int M>
+struct Rows {
+  static constexpr bool kQStage = M == 32;             // Q passes through a stage into TMEM; else it stays in shared memory
+  static constexpr int kStages = M == 32 ? 3 : 2;      // tiles in shared memory
+  static constexpr int kClears = kStages + 1;          // bf16: tiles with cleared rows that may wait for their product, and one more
+  static constexpr int kParts = 128 / M;               // threads that share a row
+  static constexpr int kCols = kT / kParts;            // keys of a thread
+  static constexpr int kDims = 256 / kParts;           // output dims of a thread in each half
+  static constexpr int kPBufs = M == 32 ? 2 : 1;       // tiles of weights
+  static constexpr int kP = M * 128;                   // M rows x 64 weights, bf16
+  static constexpr int kQSlab = M * 128;               // M rows x 64 dims of Q, bf16
+  // TMEM columns: 2 kDims of O, 2 kCols of S, and for M = 32 288 of Q
+  static constexpr uint32_t kOutCol = 0, kSCol = 2 * kDims, kQCol = kSCol + 2 * kCols;
+};
+
+template <bool FP8, bool SPARSE, int M>
 struct Cfg {
+  using R = Rows<M>;
   static constexpr int kThreads = FP8 ? 512 : 288;
   // tile descriptors in flight; a sparse one has its 64 rows' places with it
   static constexpr int kInfo = SPARSE ? 3 : 8;
-  static constexpr int kOffP = kStages * kTile;  // [2] weights of a tile
-  static constexpr int kOffX = kOffP + 2 * kP;  // [2][128] row maxima / sums
+  static constexpr int kOffQ = R::kStages * kTile;  // M = 64
+  static constexpr int kOffP = kOffQ + (R::kQStage ? 0 : 9 * R::kQSlab);
+  static constexpr int kOffX = kOffP + R::kPBufs * R::kP;  // [2][128] row maxima / sums
   static constexpr int kOffInfo = kOffX + 2 * 128 * 4;
   static constexpr int kOffSlots = kOffInfo + kInfo * static_cast<int>(sizeof(TileInfo));
   static constexpr int kOffBar = kOffSlots + (SPARSE ? kInfo * kT * 8 : 0);
   // readers of a tile descriptor: the two issuing warps, four softmax warps, and
   // the copying and the clearing warp or the widening warps
   static constexpr int kReaders = 6 + (FP8 ? 8 : 2);
-  static constexpr int kNumBars = 2 * kInfo + 2 * kStages + 11 + kClears;
+  static constexpr int kNumBars = 2 * kInfo + 2 * R::kStages + 12 + R::kClears;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16;
   static_assert(kOffBar % 8 == 0, "alignment");
@@ -106,30 +119,40 @@ IC_DEV int seq_len(const LatentArgs& a, int b) {
   return static_cast<int>(clamp_len(a, a.lens[b]));
 }
 IC_DEV int tiles_of(int len) { return (len + kT - 1) / kT; }
+// First tile of group g of G (in 32 bits where they hold it: a 64-bit division
+// costs a microsecond of the start).
+IC_DEV int64_t share_start(int g, int64_t total, int G) {
+  if (total < (1 << 22) && G < 512) return static_cast<uint32_t>(g) * static_cast<uint32_t>(total) / static_cast<uint32_t>(G);
+  return g * total / G;
+}
 IC_DEV int eff_groups(int groups, int64_t tiles) {
   const int64_t g = (tiles + kMinTiles - 1) / kMinTiles;
   return g < groups ? static_cast<int>(g) : groups;
 }
 
-template <bool FP8, bool SPARSE>
-__global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
+template <bool FP8, bool SPARSE, int M>
+__global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
     latent_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
                             const LatentArgs a) {
-  using C = Cfg<FP8, SPARSE>;
-  constexpr int kInfo = C::kInfo;
+  using C = Cfg<FP8, SPARSE, M>;
+  using R = Rows<M>;
+  constexpr int kInfo = C::kInfo, kStages = R::kStages, kClears = R::kClears, kCols = R::kCols, kDims = R::kDims;
+  constexpr uint32_t kOutCol = R::kOutCol, kSCol = R::kSCol, kQCol = R::kQCol;
+  constexpr bool kQStage = R::kQStage;
   extern __shared__ __align__(1024) uint8_t smem[];
   // the swizzled layouts need a 1024-byte-aligned base
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_status(a.status, IC_ERR_UNSUPPORTED);
     return;
   }
+  uint8_t* qs = smem + C::kOffQ;
   uint8_t* ps = smem + C::kOffP;
   float* xm = reinterpret_cast<float*>(smem + C::kOffX);
   TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kOffInfo);
   int64_t* places = reinterpret_cast<int64_t*>(smem + C::kOffSlots);  // sparse: [kInfo][64] byte offsets in the cache
   uint64_t* info_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* info_free = info_full + kInfo;
-  // the stages hold, in order, each piece's Q and its tiles
+  // the stages hold, in order, each piece's Q (M = 32) and its tiles
   uint64_t* full = info_free + kInfo;  // [kStages] Q as loaded, or a tile in operand layout
   uint64_t* freed = full + kStages;    // [kStages] Q is in TMEM, or the tile's last product has read it (bf16: and warp 8 has seen it)
   uint64_t* q_full = freed + kStages;
@@ -139,8 +162,8 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
   uint64_t* pv_done = p_ready + 2;  // [2]
   uint64_t* o_free = pv_done + 2;   // a piece's output has been read out
   uint64_t* cleared = o_free + 1;   // [kClears] bf16: a tile's rows that hold nothing are zero
-  uint64_t* xch = cleared + kClears;  // the softmax warps exchange a value
-  uint64_t* retire = xch + 1;
+  uint64_t* xch = cleared + kClears;  // [2] the softmax warps that share rows exchange a value
+  uint64_t* retire = xch + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
 
@@ -158,7 +181,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       mbar_init(&full[i], FP8 ? 8 : 1);
       mbar_init(&freed[i], FP8 ? 1 : 2);
     }
-    mbar_init(q_full, 4);
+    mbar_init(q_full, kQStage ? 4 : 1);
     mbar_init(q_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -167,7 +190,8 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     }
     mbar_init(o_free, 4);
     for (int i = 0; i < kClears; ++i) mbar_init(&cleared[i], 1);
-    mbar_init(xch, 4);
+    mbar_init(&xch[0], R::kParts);
+    mbar_init(&xch[1], R::kParts);
     mbar_init(retire, 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -203,36 +227,38 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     warp_arrive(&info_free[t % kInfo]);
     return true;
   };
-  // slab c of Q's rows of sequence b into a stage. (Rows of the next sequence, or
-  // zeros, may lie behind this one's: they are not written out.)
-  auto copy_q = [&](int b, int st, int c) {
-    tma_load_2d(smem + st * kTile + c * kQSlab, &qmap, &full[st], c * 64, b * a.rows + rb * kM);
+  // slab c of Q's rows of sequence b. (Rows of the next sequence, or zeros, may
+  // lie behind this one's: they are not written out.)
+  auto copy_q = [&](int b, uint8_t* dst, uint64_t* bar, int c) {
+    tma_load_2d(dst + c * R::kQSlab, &qmap, bar, c * 64, b * a.rows + rb * M);
   };
   const int br = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;  // rows of a TMA box
 
   if (warp == 0) {
     // ------------------------------------------------------------ tiles
+    // lane l holds the length of sequence cb + l
+    int cb = 0, clen = 0;
+    auto load_chunk = [&]() { clen = cb + lane < a.B ? seq_len<SPARSE>(a, cb + lane) : 0; };
     // this group's share of all tiles
     int64_t total = 0;
     if (SPARSE) {
       total = static_cast<int64_t>(a.B) * tiles_of(a.k);
     } else {
-      for (int b = lane; b < a.B; b += 32) {
-        const int64_t n = a.lens[b];
+      for (cb = 0; cb < a.B; cb += 32) {
+        const int64_t n = cb + lane < a.B ? a.lens[cb + lane] : 0;
         if (n != clamp_len(a, n)) record_status(a.status, IC_ERR_BAD_INDEX);
-        total += tiles_of(static_cast<int>(clamp_len(a, n)));
+        clen = static_cast<int>(clamp_len(a, n));
+        total += tiles_of(clen);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
     const int G = eff_groups(a.groups, total);
-    const int64_t g0 = group < G ? group * total / G : 0;
-    int64_t g1 = group < G ? (group + 1) * total / G : 0;
-    // lane l holds the length of sequence cb + l
-    int cb = 0, clen = 0;
+    const int64_t g0 = group < G ? share_start(group, total, G) : 0;
+    int64_t g1 = group < G ? share_start(group + 1, total, G) : 0;
+    cb = 0;
+    if (SPARSE || a.B > 32) load_chunk();  // (else the chunk is still there)
     int64_t cstart = 0;  // first tile of sequence cb
-    auto load_chunk = [&]() { clen = cb + lane < a.B ? seq_len<SPARSE>(a, cb + lane) : 0; };
-    load_chunk();
     int b = 0;            // current sequence, bstart its first tile, bt its tiles
     int64_t bstart = 0;
     int bt = 0, blen = 0;
@@ -363,7 +389,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q . K^T
-    constexpr uint32_t idesc = idesc_bf16_f32(kM, kT, false, false);
+    constexpr uint32_t idesc = idesc_bf16_f32(M, kT, false, false);
     const uint32_t ka = smem_u32(smem);
     int pieces = 0, n = 0;  // stages used so far
 #pragma unroll 1
@@ -371,11 +397,20 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       TileInfo x;
       if (!get_info(t, x) || (x.flags & kEnd)) break;
       if (x.flags & kFirst) {
-        if (!wait(q_full, pieces & 1)) break;
-        if (lane == 0) mbar_arrive(&freed[n % kStages]);
-        __syncwarp();
+        if (!kQStage) {
+          if (pieces > 0 && !wait(q_free, (pieces - 1) & 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, 9 * R::kQSlab);
+          __syncwarp();
+          if (lane < 9) copy_q(x.b, qs, q_full, lane);
+          __syncwarp();
+        }
         ++pieces;
-        ++n;
+        if (!wait(q_full, (pieces - 1) & 1)) break;
+        if (kQStage) {
+          if (lane == 0) mbar_arrive(&freed[n % kStages]);
+          __syncwarp();
+          ++n;
+        }
       }
       // the logits of tile t - 2 have been read
       if (t >= 2 && !wait(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
@@ -383,13 +418,17 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       if (!wait(&full[st], (n / kStages) & 1)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t d = tmem + kSCol + (t & 1) * 16;
-        const uint64_t bd = sw128_desc(ka + st * kTile, 16, 1024);
+        const uint32_t d = tmem + kSCol + (t & 1) * kCols;
+        const uint64_t bd = sw128_desc(ka + st * kTile, 16, 1024), ad = sw128_desc(smem_u32(qs), 16, 1024);
 #pragma unroll 1
         for (int c = 0; c < 9; ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ws_bf16_ts(d, tmem + kQCol + c * 32 + kk * 8, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (kQStage)
+              mma_ws_bf16_ts(d, tmem + kQCol + c * 32 + kk * 8, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
+            else
+              mma_ws_bf16_ss(d, ad + c * (R::kQSlab >> 4) + kk * 2, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
+          }
         mma_commit(&s_full[t & 1]);
         if (x.flags & kLast) mma_commit(q_free);
       }
@@ -400,9 +439,10 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     if (elect_one()) mma_commit(retire);
     __syncwarp();
     mbar_drain(retire, 0);
+    if (!kQStage && pieces > 0) mbar_drain(q_full, (pieces - 1) & 1);  // given up: Q lands before the CTA exits
   } else if (warp == 2) {
     // ------------------------------------------------------------ O += P . V
-    constexpr uint32_t idesc = idesc_bf16_f32(kM, 256, false, true);
+    constexpr uint32_t idesc = idesc_bf16_f32(M, 256, false, true);
     const uint32_t va = smem_u32(smem), pa = smem_u32(ps);
     int pieces = 0, nclear = 0, n = 0;
 #pragma unroll 1
@@ -413,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       if (first) {
         if (pieces > 0 && !wait(o_free, (pieces - 1) & 1)) break;
         ++pieces;
-        ++n;
+        if (kQStage) ++n;
       }
       if (!FP8 && (x.flags & kClear)) {
         if (!wait(&cleared[nclear % kClears], (nclear / kClears) & 1)) break;
@@ -424,12 +464,12 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       if (!wait(&p_ready[t & 1], (t >> 1) & 1)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t vd = sw128_desc(va + st * kTile, kSlab, 1024), pd = sw128_desc(pa + (t & 1) * kP, 16, 1024);
+        const uint64_t vd = sw128_desc(va + st * kTile, kSlab, 1024), pd = sw128_desc(pa + (t % R::kPBufs) * R::kP, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            mma_ws_bf16_ss(tmem + kOutCol + h * 64, pd + kk * 2, vd + h * (4 * kSlab >> 4) + kk * 128, idesc,
+            mma_ws_bf16_ss(tmem + kOutCol + h * kDims, pd + kk * 2, vd + h * (4 * kSlab >> 4) + kk * 128, idesc,
                            !first || kk > 0);
         mma_commit(&freed[st]);
         mma_commit(&pv_done[t & 1]);
@@ -454,9 +494,9 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       for (int t = 0;; ++t) {
         TileInfo x;
         if (!get_info(t, x) || (x.flags & kEnd)) break;
-        if (x.flags & kFirst) {
-          if (!stage(9 * kQSlab)) break;
-          if (lane < 9) copy_q(x.b, n % kStages, lane);
+        if (kQStage && (x.flags & kFirst)) {
+          if (!stage(9 * R::kQSlab)) break;
+          if (lane < 9) copy_q(x.b, smem + (n % kStages) * kTile, &full[n % kStages], lane);
           __syncwarp();
           ++n;
         }
@@ -481,31 +521,33 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ Q, softmax and output
-    // Thread (quadrant, lane) has query row `lane` of the block and a quarter
-    // of the columns: 16 of a tile's keys, 128 of the output dims.
     const int quad = warp & 3;
+    const int part = M == 32 ? quad : quad >> 1;  // of the columns: kCols of a tile's keys, kDims of each half of the output
+    const int r = M == 32 ? lane : (quad & 1) * 32 + lane;  // query row of the block
     const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float c2 = a.sm_scale * kLog2e;
-    const int row = rb * kM + lane;          // query row of the sequence
+    const int row = rb * M + r;              // query row of the sequence
     const bool live = row < a.rows;
     const int back = a.Q - 1 - (live ? row / a.H : 0);  // the row's token ends this many positions before the last
     const float sink2 = a.sink && live ? a.sink[row % a.H] * kLog2e : -INFINITY;
     float ref = -INFINITY, l = 0.f;
     uint32_t nx = 0;  // exchanges so far
+    uint64_t* const xbar = &xch[M == 32 ? 0 : quad & 1];
     auto offer = [&](float v) {
       xm[(nx & 1) * 128 + quad * 32 + lane] = v;
-      warp_arrive(xch);
+      warp_arrive(xbar);
     };
-    auto take = [&](float (&v)[4]) {
-      const bool ok = wait(xch, nx & 1);
+    auto take = [&](float (&v)[R::kParts]) {  // the values of the row's parts
+      const bool ok = wait(xbar, nx & 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = xm[(nx & 1) * 128 + i * 32 + lane];
+      for (int i = 0; i < R::kParts; ++i) v[i] = xm[(nx & 1) * 128 + (M == 32 ? i : (quad & 1) + 2 * i) * 32 + lane];
       ++nx;
       return ok;
     };
     // Q of a piece from its stage into the quadrant's copy in TMEM
     int n = 0;
     auto load_q = [&]() {
+      if (!kQStage) return true;
       if (!wait(&full[n % kStages], (n / kStages) & 1)) return false;
       const uint8_t* src = smem + (n % kStages) * kTile;
 #pragma unroll 1
@@ -513,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
         uint32_t v[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(src + c * kQSlab + sw128_offset(lane, i));
+          const uint4 w = *reinterpret_cast<const uint4*>(src + c * R::kQSlab + sw128_offset(lane, i));
           v[4 * i] = w.x;
           v[4 * i + 1] = w.y;
           v[4 * i + 2] = w.z;
@@ -536,33 +578,34 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       ok = wait(&s_full[t & 1], (t >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t rv[16];
-      tmem_ld16_issue(tlane + kSCol + (t & 1) * 16, rv);
+      uint32_t rv[kCols];
+      tmem_ld_issue(tlane + kSCol + (t & 1) * kCols, rv);
       if (x.flags & kFirst) {
         ref = -INFINITY;
         l = 0.f;
       }
-      uint32_t mask = ((quad & 2 ? x.mask[1] : x.mask[0]) >> ((quad & 1) * 16)) & 0xffffu;
-      const int seen = x.len - back - (x.pos0 + quad * 16);  // columns of this thread before the row's limit
-      if (seen < 16) mask = seen <= 0 ? 0u : mask & ((1u << seen) - 1);
-      tmem_ld_wait16(rv);
-      if (!__all_sync(0xffffffffu, mask == 0xffffu)) {
+      constexpr uint32_t kAll = kCols == 32 ? 0xffffffffu : (1u << kCols) - 1;
+      uint32_t mask = ((part * kCols & 32 ? x.mask[1] : x.mask[0]) >> (part * kCols & 31)) & kAll;
+      const int seen = x.len - back - (x.pos0 + part * kCols);  // columns of this thread before the row's limit
+      if (seen < kCols) mask = seen <= 0 ? 0u : mask & ((1u << seen) - 1);
+      tmem_ld_wait_for(rv);
+      if (!__all_sync(0xffffffffu, mask == kAll)) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < kCols; ++j)
           if (!((mask >> j) & 1u)) rv[j] = 0xff800000u;  // -inf
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(rv[j]));
+      for (int j = 0; j < kCols; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(rv[j]));
       offer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
       // The sum is of the 32-bit weights; those of the product are rounded to
       // bf16 (2^-8 of each at most, of either sign), as the MMA takes them.
-      uint32_t pk[8];
+      uint32_t pk[kCols / 2];
       float sum = 0.f;
       auto weigh = [&](float base) {
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
+        for (int j = 0; j < kCols; j += 2) {
           const float p0 = ex2_approx(fmaf(__uint_as_float(rv[j]), c2, -base));
           const float p1 = ex2_approx(fmaf(__uint_as_float(rv[j + 1]), c2, -base));
           part[(j >> 1) & 3] += p0 + p1;
@@ -570,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
         }
         sum = (part[0] + part[1]) + (part[2] + part[3]);
       };
-      // First under the old reference, while the other quarters' maxima come
+      // First under the old reference, while the other parts' maxima come
       // (most tiles leave it where it is), and again if it has moved. (A row
       // with nothing valid so far: every weight is 0.)
       float scale = 1.f;
@@ -578,9 +621,12 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       for (int pass = 0;; ++pass) {
         weigh(ref == -INFINITY ? 0.f : ref);
         if (pass) break;
-        float other[4];
+        float other[R::kParts];
         ok = take(other);
-        const float m = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3])) * c2;
+        float m = other[0];
+#pragma unroll
+        for (int i = 1; i < R::kParts; ++i) m = fmaxf(m, other[i]);
+        m *= c2;
         // the reference moves when the row's maximum passes it by more than
         // kMove: weights stay below 2^8, far from bf16's and fp32's limits
         bool moved = false;
@@ -596,15 +642,15 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       }
       if (!ok) break;
       l = fmaf(l, scale, sum);
-      // the product of two tiles ago has read its weights
-      if (t >= 2) ok = wait(&pv_done[t & 1], ((t >> 1) - 1) & 1);
+      // the product that used this buffer has read its weights
+      if (t >= R::kPBufs) ok = wait(&pv_done[(t - R::kPBufs) & 1], ((t - R::kPBufs) >> 1) & 1);
       if (!ok) break;
-      if (__any_sync(0xffffffffu, scale != 1.f)) {  // (then t > 0, and the four warps agree)
+      if (__any_sync(0xffffffffu, scale != 1.f)) {  // (then t > 0, and the warps of a row agree)
         ok = wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);  // O stands still
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2 * kDims / 32; ++c) {
           uint32_t o[32];
           tmem_ld32_issue(tlane + kOutCol + c * 32, o);
           tmem_ld_wait(o);
@@ -614,10 +660,10 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
         }
         tmem_st_wait();
       }
-      const uint32_t pb = smem_u32(ps + (t & 1) * kP);
+      const uint32_t pb = smem_u32(ps + (t % R::kPBufs) * R::kP);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        st_shared_v4(pb + sw128_offset(lane, quad * 2 + i),
+      for (int i = 0; i < kCols / 8; ++i)
+        st_shared_v4(pb + sw128_offset(r, part * (kCols / 8) + i),
                      make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
       fence_proxy_async_smem();
       tc_fence_before();
@@ -627,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       if (!ok) break;
       if (!(y.flags & kLast)) continue;
       // ---- Q of the next piece, and this one's output
-      if (!(x.flags & kEnd)) {
+      if (kQStage && !(x.flags & kEnd)) {
         ok = wait(q_free, pieces & 1);
         if (!ok) break;
         tc_fence_after();
@@ -636,35 +682,37 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
       }
       ++pieces;
       offer(l);
-      float ls[4];
+      float ls[R::kParts];
       ok = take(ls) && wait(&pv_done[t & 1], (t >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      float lsum = ls[0];
+#pragma unroll
+      for (int i = 1; i < R::kParts; ++i) lsum += ls[i];
       const bool whole = (y.flags & kWhole) != 0;
       const int64_t gr = (static_cast<int64_t>(y.b) * a.rows) + row;
-      const int64_t pr = (static_cast<int64_t>(y.slot) * a.rblocks + rb) * kM + lane;
+      const int64_t pb0 = static_cast<int64_t>(y.slot) * a.rblocks + rb;  // block of partials
       float f = 1.f;
       if (whole) {
-        const float M = fmaxf(ref, sink2);
-        const float w = ref == -INFINITY ? 0.f : exp2f(ref - M);
-        const float den = lsum * w + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - M));
+        const float top = fmaxf(ref, sink2);
+        const float w = ref == -INFINITY ? 0.f : exp2f(ref - top);
+        const float den = lsum * w + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - top));
         f = w > 0.f ? w / den : 0.f;
-        if (live && quad == 0 && a.lse) a.lse[gr] = M == -INFINITY ? -INFINITY : (M + log2f(den)) / kLog2e;
-      } else if (quad == 0) {
-        a.part_ml[pr * 2] = ref;
-        a.part_ml[pr * 2 + 1] = lsum;
+        if (live && part == 0 && a.lse) a.lse[gr] = top == -INFINITY ? -INFINITY : (top + log2f(den)) / kLog2e;
+      } else if (part == 0) {
+        reinterpret_cast<float2*>(a.part_ml)[pb0 * M + r] = make_float2(ref, lsum);
       }
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2 * kDims / 32; ++c) {
         uint32_t o[32];
         tmem_ld32_issue(tlane + kOutCol + c * 32, o);
         tmem_ld_wait(o);
-        const int dim = (c >> 1) * 256 + quad * 64 + (c & 1) * 32;
+        const int dim = c / (kDims / 32) * 256 + part * kDims + c % (kDims / 32) * 32;
         if (!whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + pr * 512 + dim);
+          // [block][dim / 4][row][4]: a warp's rows side by side
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + (pb0 * 128 + dim / 4) * M + r;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 8; ++k) dst[k * M] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else if (live) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
@@ -710,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     for (int t = 0;; ++t, ++n) {
       TileInfo x;
       if (!get_info(t, x) || (x.flags & kEnd)) break;
-      if (x.flags & kFirst) {
+      if (kQStage && (x.flags & kFirst)) {
         if (!landed()) break;
         warp_arrive(&freed[n % kStages]);
         ++n;
@@ -784,17 +832,17 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     for (int u = 0; more; ++u) {
       const int t = u >> 1, h = u & 1;
       if (h == 0) {
-        if (first) {  // the first of these warps copies Q
+        if (kQStage && first) {  // the first of these warps copies Q
           if (w == 0) {
             const int qs = n % kStages;
             ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
             if (!ok) break;
             if (lane == 0) {
               mbar_arrive_n(&full[qs], 7);
-              mbar_arrive_expect_tx(&full[qs], 9 * kQSlab);
+              mbar_arrive_expect_tx(&full[qs], 9 * R::kQSlab);
             }
             __syncwarp();
-            if (lane < 9) copy_q(b, qs, lane);
+            if (lane < 9) copy_q(b, smem + qs * kTile, &full[qs], lane);
             __syncwarp();
             qn = n;
           }
@@ -858,18 +906,23 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
 }
 
 // Joins the pieces of each sequence that more than one group worked on, and
-// writes the rows of sequences without a tile. WPR warps share a row's pieces;
-// lane l has dims 128 i + 4 l + [0, 4), i < 4.
+// writes the rows of sequences without a tile. A warp has 32 query rows, one a
+// lane, and 16 output dims; its reads of the partials, [dim / 4][row][4], are
+// 512 bytes in a row. WPP warps share the pieces of one such part, each with its
+// own running reference.
 constexpr int kJoinThreads = 256;
-template <bool SPARSE, int WPR>
+template <bool SPARSE, int M, int WPP>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentArgs a) {
-  constexpr int RPC = 8 / WPR;  // rows of a CTA
+  constexpr int kPerCta = 8 / WPP;       // parts of a CTA
+  constexpr int kCtas = 32 / kPerCta;    // CTAs of 32 rows
   __shared__ int64_t sums[2][8];
-  __shared__ float4 accs[WPR > 1 ? 8 : 1][128];
+  __shared__ float4 accs[WPP > 1 ? 8 : 1][4][32];
+  __shared__ float2 mls[WPP > 1 ? 8 : 1][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_seq = (a.rows + RPC - 1) / RPC;
-  const int b = blockIdx.x / per_seq;
-  const int row = (blockIdx.x - b * per_seq) * RPC + warp / WPR;
+  const int row32 = (a.rows + 31) / 32;
+  const int b = blockIdx.x / (row32 * kCtas), rest = blockIdx.x - b * row32 * kCtas;
+  const int row = rest / kCtas * 32 + lane;
+  const int dim = (rest % kCtas * kPerCta + warp / WPP) * 16;
   pdl_trigger();
   pdl_wait();
   // tiles of all sequences, and of those before b
@@ -880,12 +933,12 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
     total = static_cast<int64_t>(a.B) * bt;
     start = static_cast<int64_t>(b) * bt;
   } else {
+    bt = tiles_of(seq_len<SPARSE>(a, b));
     for (int i = threadIdx.x; i < a.B; i += kJoinThreads) {
       const int n = tiles_of(seq_len<SPARSE>(a, i));
       total += n;
       if (i < b) start += n;
     }
-    bt = tiles_of(seq_len<SPARSE>(a, b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -897,132 +950,146 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
     }
     __syncthreads();
     total = start = 0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
       total += sums[0][i];
       start += sums[1][i];
     }
   }
-  int gf = 0, gl = -1;
+  int gf = 0, gl = -1, first_slot = 0;
   const int G = eff_groups(a.groups, total);
   if (bt > 0) {
-    gf = static_cast<int>(((start + 1) * G - 1) / total);  // the group of the first tile, and of the last
-    gl = static_cast<int>(((start + bt) * G - 1) / total);
+    // the group of the first tile, and of the last
+    if (total < (1 << 22) && G < 512) {
+      gf = static_cast<int>((static_cast<uint32_t>(start + 1) * static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(total));
+      gl = static_cast<int>((static_cast<uint32_t>(start + bt) * static_cast<uint32_t>(G) - 1) / static_cast<uint32_t>(total));
+    } else {
+      gf = static_cast<int>(((start + 1) * G - 1) / total);
+      gl = static_cast<int>(((start + bt) * G - 1) / total);
+    }
     if (gf == gl) return;  // one piece: written already
+    // only the first of the groups may hold another sequence before this one
+    first_slot = share_start(gf, total, G) < start ? 1 : 0;
   }
   const bool live = row < a.rows;
-  const int rb = row / kM, r = row % kM;
-  // only the first of the groups may hold another sequence before this one
-  const int first_slot = bt > 0 && gf * total / G < start ? 1 : 0;
-  auto part_row = [&](int g) {
-    const int slot = 2 * g + (g == gf ? first_slot : 0);
-    return (static_cast<int64_t>(slot) * a.rblocks + rb) * kM + r;
-  };
-  const float sink2 = a.sink && live ? a.sink[row % a.H] * kLog2e : -INFINITY;
-  float M = sink2, den = 0.f;
+  const int rb = row / M, r = row % M;
+  float m = -INFINITY, den = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (live) {
-    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-    for (int g = gf + lane; g <= gl; g += 32) M = fmaxf(M, ml[part_row(g)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int g = gf + lane; g <= gl; g += 32) {
-      const float2 v = ml[part_row(g)];
-      if (v.x != -INFINITY) den = fmaf(exp2f(v.x - M), v.y, den);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (sink2 != -INFINITY) den += exp2f(sink2 - M);
-#pragma unroll 2
-    for (int g = gf + warp % WPR; g <= gl; g += WPR) {
-      const int64_t pr = part_row(g);
-      const float m = ml[pr].x;
-      const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + pr * 512) + lane;
+#pragma unroll 4
+    for (int g = gf + warp % WPP; g <= gl; g += WPP) {
+      const int64_t block = static_cast<int64_t>(2 * g + (g == gf ? first_slot : 0)) * a.rblocks + rb;
+      const float2 v = reinterpret_cast<const float2*>(a.part_ml)[block * M + r];
+      const float4* src = reinterpret_cast<const float4*>(a.part_o) + (block * 128 + dim / 4) * M + r;
+      const float4 p[4] = {src[0], src[M], src[2 * M], src[3 * M]};
+      const float top = fmaxf(m, v.x);
+      const float keep = m == -INFINITY ? 0.f : ex2_approx(m - top), w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - top);
+      m = top;
+      den = fmaf(den, keep, w * v.y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = src[32 * i];
-        acc[i].x = fmaf(w, v.x, acc[i].x);
-        acc[i].y = fmaf(w, v.y, acc[i].y);
-        acc[i].z = fmaf(w, v.z, acc[i].z);
-        acc[i].w = fmaf(w, v.w, acc[i].w);
+        acc[i].x = fmaf(acc[i].x, keep, w * p[i].x);
+        acc[i].y = fmaf(acc[i].y, keep, w * p[i].y);
+        acc[i].z = fmaf(acc[i].z, keep, w * p[i].z);
+        acc[i].w = fmaf(acc[i].w, keep, w * p[i].w);
       }
     }
   }
-  if constexpr (WPR > 1) {
+  if constexpr (WPP > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) accs[warp][32 * i + lane] = acc[i];
+    for (int i = 0; i < 4; ++i) accs[warp][i][lane] = acc[i];
+    mls[warp][lane] = make_float2(m, den);
     __syncthreads();
-    if (warp % WPR) return;
-    for (int k = 1; k < WPR; ++k)
+    if (warp % WPP) return;
+#pragma unroll 1
+    for (int k = 1; k < WPP; ++k) {
+      const float2 v = mls[warp + k][lane];
+      const float top = fmaxf(m, v.x);
+      const float keep = m == -INFINITY ? 0.f : ex2_approx(m - top), w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - top);
+      m = top;
+      den = fmaf(den, keep, w * v.y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = accs[warp + k][32 * i + lane];
-        acc[i].x += v.x;
-        acc[i].y += v.y;
-        acc[i].z += v.z;
-        acc[i].w += v.w;
+        const float4 p = accs[warp + k][i][lane];
+        acc[i].x = fmaf(acc[i].x, keep, w * p.x);
+        acc[i].y = fmaf(acc[i].y, keep, w * p.y);
+        acc[i].z = fmaf(acc[i].z, keep, w * p.z);
+        acc[i].w = fmaf(acc[i].w, keep, w * p.w);
       }
+    }
   }
   if (!live) return;
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float sink2 = a.sink ? a.sink[row % a.H] * kLog2e : -INFINITY;
+  const float top = fmaxf(m, sink2);
+  const float w = m == -INFINITY ? 0.f : exp2f(m - top);
+  den = den * w + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - top));
+  const float f = w > 0.f ? w / den : 0.f;
   const int64_t gr = static_cast<int64_t>(b) * a.rows + row;
+  float o[16];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float o[4] = {acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv};
-    const int dim = 128 * i + 4 * lane;
-    if (a.gate) {
-      const uint2 g = *reinterpret_cast<const uint2*>(a.gate + gr * 512 + dim);
-      const uint32_t gw[2] = {g.x, g.y};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] *= __fdividef(1.f, 1.f + ex2_approx(-kLog2e * bf16_lane(gw[e >> 1], e & 1)));
-    }
-    if (a.out_f32)
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + gr * 512 + dim) = make_float4(o[0], o[1], o[2], o[3]);
-    else
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + gr * 512 + dim) =
-          make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    o[4 * i] = acc[i].x * f;
+    o[4 * i + 1] = acc[i].y * f;
+    o[4 * i + 2] = acc[i].z * f;
+    o[4 * i + 3] = acc[i].w * f;
   }
-  if (a.lse && lane == 0) a.lse[gr] = M == -INFINITY ? -INFINITY : (M + log2f(den)) / kLog2e;
+  if (a.gate) {
+    const uint4* g = reinterpret_cast<const uint4*>(a.gate + gr * 512 + dim);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 v = g[k];
+      const uint32_t gw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[8 * k + e] *= __fdividef(1.f, 1.f + ex2_approx(-kLog2e * bf16_lane(gw[e >> 1], e & 1)));
+    }
+  }
+  if (a.out_f32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + gr * 512 + dim);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + gr * 512 + dim);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                          pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+  }
+  if (a.lse && dim == 0) a.lse[gr] = top == -INFINITY ? -INFINITY : (top + log2f(den)) / kLog2e;
 }
 
-template <bool FP8, bool SPARSE>
-cudaError_t launch_main(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, cudaStream_t stream) {
-  using C = Cfg<FP8, SPARSE>;
-  auto kern = latent_attention_kernel<FP8, SPARSE>;
+template <bool FP8, bool SPARSE, int M>
+cudaError_t launch_m(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, cudaStream_t stream) {
+  using C = Cfg<FP8, SPARSE, M>;
+  auto kern = latent_attention_kernel<FP8, SPARSE, M>;
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(static_cast<unsigned>(a.groups) * a.rblocks), dim3(C::kThreads), C::kSmemBytes,
-                       stream, false, qmap, kvmap, a);
-}
-
-template <bool SPARSE>
-cudaError_t launch_join(const LatentArgs& a, cudaStream_t stream) {
+  e = launch_kernel(kern, dim3(static_cast<unsigned>(a.groups) * a.rblocks), dim3(C::kThreads), C::kSmemBytes, stream,
+                    false, qmap, kvmap, a);
+  if (e != cudaSuccess) return e;
   // pieces of a sequence: about groups / B + 1
-  const int pieces = a.groups / a.B + 1;
-  const int wpr = pieces <= 2 ? 1 : pieces <= 8 ? 4 : 8;
-  const int rpc = 8 / wpr;
-  const dim3 grid(static_cast<unsigned>(a.B) * ((a.rows + rpc - 1) / rpc));
-  auto kern = wpr == 1 ? latent_join_kernel<SPARSE, 1>
-                       : wpr == 4 ? latent_join_kernel<SPARSE, 4> : latent_join_kernel<SPARSE, 8>;
-  return launch_kernel(kern, grid, dim3(kJoinThreads), 0, stream, true, a);
+  const bool many = a.groups / a.B + 1 > 4;
+  const unsigned ctas = static_cast<unsigned>(a.B) * ((a.rows + 31) / 32) * (many ? 32 : 4);
+  auto join = many ? latent_join_kernel<SPARSE, M, 8> : latent_join_kernel<SPARSE, M, 1>;
+  return launch_kernel(join, dim3(ctas), dim3(kJoinThreads), 0, stream, true, a);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_attention(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, bool fp8,
                                     bool sparse, cudaStream_t stream, int* launches) {
-  cudaError_t e = sparse ? launch_main<true, true>(qmap, kvmap, a, stream)
-                  : fp8  ? launch_main<true, false>(qmap, kvmap, a, stream)
-                         : launch_main<false, false>(qmap, kvmap, a, stream);
-  if (e != cudaSuccess) return e;
-  e = sparse ? launch_join<true>(a, stream) : launch_join<false>(a, stream);
-  if (e != cudaSuccess) return e;
-  *launches += 2;
-  return cudaGetLastError();
+  const bool m32 = a.block == 32;
+  const cudaError_t e = sparse ? (m32 ? launch_m<true, true, 32>(qmap, kvmap, a, stream)
+                                      : launch_m<true, true, 64>(qmap, kvmap, a, stream))
+                        : fp8  ? (m32 ? launch_m<true, false, 32>(qmap, kvmap, a, stream)
+                                      : launch_m<true, false, 64>(qmap, kvmap, a, stream))
+                               : (m32 ? launch_m<false, false, 32>(qmap, kvmap, a, stream)
+                                      : launch_m<false, false, 64>(qmap, kvmap, a, stream));
+  if (e == cudaSuccess) *launches += 2;
+  return e;
 }
 
 }  // namespace ic
