@@ -215,6 +215,8 @@ IC_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 IC_DEV void bulk_prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
+// Ask L2 for the line of an address.
+IC_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 // Shared -> global tile store of a 4-D tensor map (bulk-group completion);
 // rows outside the map's extent are not written.
 IC_DEV void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {

@@ -227,10 +227,15 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
     warp_arrive(&info_free[t % kInfo]);
     return true;
   };
-  // slab c of Q's rows of sequence b. (Rows of the next sequence, or zeros, may
-  // lie behind this one's: they are not written out.)
-  auto copy_q = [&](int b, uint8_t* dst, uint64_t* bar, int c) {
-    tma_load_2d(dst + c * R::kQSlab, &qmap, bar, c * 64, b * a.rows + rb * M);
+  // Q's rows of sequence b, by one warp. (Rows of the next sequence, or zeros,
+  // may lie behind this one's: they are not written out.) One elected lane
+  // issues the copies: lanes that issue their own cost about 100 cycles each.
+  auto copy_q = [&](int b, uint8_t* dst, uint64_t* bar) {
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < 9; ++c) tma_load_2d(dst + c * R::kQSlab, &qmap, bar, c * 64, b * a.rows + rb * M);
+    }
+    __syncwarp();
   };
   const int br = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;  // rows of a TMA box
 
@@ -326,7 +331,9 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
           }
           const int page = s / a.page_size;
           const int64_t at = page * a.page_stride + static_cast<int64_t>(s - page * a.page_size) * kLatentRowFp8;
-          bulk_prefetch_l2(a.cache + at, kLatentRowFp8);
+#pragma unroll
+          for (int i = 0; i < kLatentRowFp8; i += 128) prefetch_l2(a.cache + at + i);
+          prefetch_l2(a.cache + at + kLatentRowFp8 - 16);
           return at;
         };
         s0 = find(pos0 + lane);
@@ -336,6 +343,8 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
       } else {
         const int p = pos0 + lane * unit;
         int rows = 0;  // valid rows of the unit
+        int64_t ahead = 0;
+        uint32_t ahead_bytes = 0;
         if (lane * unit < kT && p < blen) {
           const int pi = p / a.page_size;
           const int page = a.table[static_cast<int64_t>(b) * a.table_stride + pi];
@@ -344,10 +353,19 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
             constexpr int kRow = FP8 ? kLatentRowFp8 : kLatentRowBf16;
             const int64_t byte = page * a.page_stride + static_cast<int64_t>(p - pi * a.page_size) * kRow;
             src = FP8 ? byte : page;
-            bulk_prefetch_l2(a.cache + byte, static_cast<uint32_t>(rows * kRow));
+            ahead = byte;
+            ahead_bytes = static_cast<uint32_t>(rows * kRow);
           } else {
             record_status(a.status, IC_ERR_BAD_INDEX);
           }
+        }
+        // ask L2 for the units
+#pragma unroll 1
+        for (int i = 0; i * unit < kT; ++i) {
+          const int64_t from = __shfl_sync(0xffffffffu, ahead, i);
+          const uint32_t bytes = __shfl_sync(0xffffffffu, ahead_bytes, i);
+          if (bytes && elect_one()) bulk_prefetch_l2(a.cache + from, bytes);
+          __syncwarp();
         }
         // bit r of the mask: row r is in a valid unit, before the end
         const int rows_of = __shfl_sync(0xffffffffu, rows, lane / unit);
@@ -401,8 +419,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
           if (pieces > 0 && !wait(q_free, (pieces - 1) & 1)) break;
           if (lane == 0) mbar_arrive_expect_tx(q_full, 9 * R::kQSlab);
           __syncwarp();
-          if (lane < 9) copy_q(x.b, qs, q_full, lane);
-          __syncwarp();
+          copy_q(x.b, qs, q_full);
         }
         ++pieces;
         if (!wait(q_full, (pieces - 1) & 1)) break;
@@ -496,21 +513,25 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
         if (!get_info(t, x) || (x.flags & kEnd)) break;
         if (kQStage && (x.flags & kFirst)) {
           if (!stage(9 * R::kQSlab)) break;
-          if (lane < 9) copy_q(x.b, smem + (n % kStages) * kTile, &full[n % kStages], lane);
-          __syncwarp();
+          copy_q(x.b, smem + (n % kStages) * kTile, &full[n % kStages]);
           ++n;
         }
         if (!stage(kTile)) break;
-        // lane l has box l of each slab; boxes without a valid row read the
-        // page behind the last, which fills zeros
-        const int64_t page = lane == 0 ? x.at[0] : lane == 1 ? x.at[1] : lane == 2 ? x.at[2] : x.at[3];
-        const int pz = page < 0 ? a.num_pages : static_cast<int>(page);
-        const int py = (x.row0 + lane * br) % a.page_size;
-        if (lane * br < kT)
-#pragma unroll 1
-          for (int c = 0; c < 9; ++c)
-            tma_load_3d(smem + (n % kStages) * kTile + c * kSlab + lane * br * 128, &kvmap, &full[n % kStages], c * 64,
-                        py, pz);
+        // boxes without a valid row read the page behind the last, which fills zeros
+        if (elect_one()) {
+          uint8_t* dst = smem + (n % kStages) * kTile;
+          int py = x.row0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i * br >= kT) break;
+            const int pz = x.at[i] < 0 ? a.num_pages : static_cast<int>(x.at[i]);
+#pragma unroll
+            for (int c = 0; c < 9; ++c)
+              tma_load_3d(dst + c * kSlab + i * br * 128, &kvmap, &full[n % kStages], c * 64, py, pz);
+            py += br;
+            if (py >= a.page_size) py = 0;
+          }
+        }
         __syncwarp();
         ++n;
       }
@@ -767,9 +788,9 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
       const int st = n % kStages;
       if (x.flags & kClear) {
         const uint32_t base = smem_u32(smem) + st * kTile + (lane >> 3) * kSlab + (lane & 7) * 16;
-#pragma unroll 1
+#pragma unroll 8
         for (int r = 0; r < kT; ++r)
-          if (!((x.mask[r >> 5] >> (r & 31)) & 1u)) {
+          if (!(((r & 32 ? x.mask[1] : x.mask[0]) >> (r & 31)) & 1u)) {
             st_shared_v4(base + r * 128, make_uint4(0, 0, 0, 0));
             st_shared_v4(base + 4 * kSlab + r * 128, make_uint4(0, 0, 0, 0));
           }
@@ -842,8 +863,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
               mbar_arrive_expect_tx(&full[qs], 9 * R::kQSlab);
             }
             __syncwarp();
-            if (lane < 9) copy_q(b, smem + qs * kTile, &full[qs], lane);
-            __syncwarp();
+            copy_q(b, smem + qs * kTile, &full[qs]);
             qn = n;
           }
           ++n;
