@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexcache.so")
 SOURCES = ["api.cu", "indexer.cu", "topk.cu", "sparse_mla.cu", "topk_noalloc.cu", "append.cu", "gate.cu", "context_parallel.cu", "topk_threshold.cu", "overlap.cu",
-           "rope.cu", "latent_cache.cu", "latent_attention.cu"]
+           "rope.cu", "latent_cache.cu", "latent_attention.cu", "latent_pair.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-diag-suppress", "177", "-I", INCLUDE]

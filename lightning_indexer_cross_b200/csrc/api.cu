@@ -434,6 +434,7 @@ struct LatentLayout {
 LatentLayout latent_layout(int64_t B, int64_t rows, int64_t max_len) {
   LatentLayout L{};
   L.rblocks = static_cast<int>(ceil_div<int64_t>(rows, ic::latent_block(rows)));
+  if (ic::latent_pair(rows)) L.rblocks = (L.rblocks + 1) & ~1;
   L.groups = latent_groups(B * ceil_div<int64_t>(max_len, ic::kLatentTile), L.rblocks);
   const size_t pieces = size_t(2) * L.groups * L.rblocks * ic::latent_block(rows);
   L.o_off = kStatusBytes;
@@ -476,7 +477,7 @@ ic_status_t latent_impl(const void* q, const void* cache, ic_dtype_t dtype, int6
   }
   CUtensorMap kvmap = qmap;  // e4m3 pages are read without a map
   if (!fp8) {
-    const cuuint32_t br = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+    const cuuint32_t br = page_size % 64 == 0 && !ic::latent_pair(rows) ? 64 : page_size % 32 == 0 ? 32 : 16;
     const cuuint64_t dims[3] = {576, static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(num_pages)};
     const cuuint64_t strides[2] = {ic::kLatentRowBf16, static_cast<cuuint64_t>(page_stride)};
     const cuuint32_t box[3] = {64, br, 1};

@@ -265,8 +265,9 @@ cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t s
 
 // ---------------------------------------------------------------- attention over the paged latent cache
 constexpr int kLatentTile = 64;  // keys of a tile
-// Query rows of a CTA.
+// Query rows of a CTA, and whether two CTAs of 64 work as a pair.
 inline int latent_block(int64_t rows) { return rows <= 32 ? 32 : 64; }
+inline bool latent_pair(int64_t rows) { return rows > 64; }
 
 struct LatentArgs {
   const uint8_t* cache;
@@ -281,7 +282,7 @@ struct LatentArgs {
   int B, Q, H;
   int rows;              // Q * H query rows of a sequence
   int block;             // query rows of a CTA (latent_block)
-  int rblocks;           // ceil(rows / block)
+  int rblocks;           // ceil(rows / block), even for pairs
   int groups;            // shares of the tiles; groups * rblocks CTAs
   const float* sink;     // [H] or null
   const __nv_bfloat16* gate;  // [B, Q, H, 512] or null
@@ -294,11 +295,15 @@ struct LatentArgs {
   int* status;
   uint64_t wait_ns;
 };
-// kvmap (bf16 pages): 3-D map (576, page_size, num_pages), box 64 x box_rows x 1,
-// 128-byte swizzle; e4m3 pages are copied without a map (any valid map).
+// kvmap (bf16 pages): 3-D map (576, page_size, num_pages), box 64 x box_rows x 1
+// (box_rows: the largest of 64, 32, 16 that divides page_size; at most 32 for
+// pairs), 128-byte swizzle; e4m3 pages are copied without a map (any valid map).
 // qmap: 2-D map over q as [B * rows, 576] bf16, box 64 x block, 128-byte swizzle.
 cudaError_t launch_latent_attention(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, bool fp8,
                                     bool sparse, cudaStream_t stream, int* launches);
+// The main kernel for pairs; the joining one follows it.
+cudaError_t launch_latent_pair(const CUtensorMap& qmap, const CUtensorMap& kvmap, const LatentArgs& a, bool fp8,
+                               bool sparse, cudaStream_t stream);
 
 // ---------------------------------------------------------------- output gate
 struct GateArgs {
