@@ -24,8 +24,8 @@
 // both; what they wait for (Q, keys, values, weights) is told to its barriers by
 // both CTAs, and their commits tell both. bf16 pages: warp 3 copies, warp 8 sees
 // the copies land, clears the rows behind a sequence's end and passes the tile
-// on. e4m3 pages: warps 8-15 widen their CTA's 32 keys once and store them as
-// keys here, and as values here and in the other CTA.
+// on. e4m3 pages: warps 8-15 widen their CTA's 32 keys, and the other's for its
+// own 256 dims.
 #include "latent.cuh"
 
 namespace ic {
@@ -90,20 +90,11 @@ IC_DEV void commit_pair(uint64_t* bar) {
 }
 // Arrive on a barrier of either CTA. What it tells of are writes to this CTA's
 // memory that fence.proxy.async has handed to the tensor core, or copies that
-// have landed; the form with a release at cluster scope (1000 cycles, measured)
-// is for writes to the other CTA's memory.
+// have landed. (A release at cluster scope costs 1000 cycles, measured.)
 IC_DEV void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-IC_DEV void arrive_cluster_release(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-IC_DEV void st_cluster_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-// Generic writes to shared memory of either CTA, before the tensor core reads them.
-IC_DEV void fence_proxy_async_pair() { asm volatile("fence.proxy.async.shared::cluster;" ::: "memory"); }
+
 template <bool FP8, bool SPARSE>
 __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
     latent_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
@@ -361,22 +352,27 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
     }
   } else if (FP8 && warp >= 8) {
     // ------------------------------------------------------------ widening (e4m3)
-    // Warp w has four of this CTA's 32 keys of the tile; a load takes a whole
-    // row's codes, lane l the 16 of word l. They are stored twice: as keys, and
-    // as values in the CTA that has their dims (lanes 0-15: the first). Eight
-    // lanes that store together have four words of two neighbouring slabs; those
-    // of the odd slab store their second half first, so the eight meet eight
-    // chunks of the swizzle. The next tile's loads are in flight while one is
-    // widened.
+    // Warp w has four of this CTA's 32 keys of the tile: a load takes a whole
+    // row's codes, lane l the 16 of word l, and they are stored as keys, and those
+    // of this CTA's 256 output dims as values too. The same four of the other
+    // CTA's keys are read for those dims alone, two rows a load. (Sent across the
+    // pair instead, they cost a fence and a release at cluster scope, 2000 cycles a
+    // tile against 300 for widening them here.) Eight lanes that store together
+    // have four words of two neighbouring slabs; those of the odd slab store their
+    // second half first, so the eight meet eight chunks of the swizzle. The next
+    // tile's loads are in flight while one is widened.
     const int w = warp - 8;
     struct Unit {
-      uint4 code[4], rot;  // rot: word lane & 7 of row lane >> 3
-      float scale;         // lane l < 16: group l & 3 of row l >> 2
+      uint4 code[4], rot;   // rot: word lane & 7 of row lane >> 3
+      uint4 far[2];         // word lane & 15 of this CTA's dims of the other CTA's row 2 i + (lane >> 4)
+      float scale;          // lane l < 16: group l & 3 of row l >> 2
+      float far_scale;      // lane l < 8: group 2 rank + (l & 1) of the other CTA's row l >> 1
     } cur, nxt;
     const int odd = (lane >> 2) & 1, wch = lane & 3;
     const int r0 = 4 * w;  // first of the warp's rows among the 32
-    const uint32_t vto = dsmem_addr(vs, lane >> 4) + ((lane >> 2) & 3) * kSlab;
+    const uint32_t vto = smem_u32(vs) + ((lane >> 2) & 3) * kSlab;
     const uint32_t kto = smem_u32(ks) + (lane >> 2) * 4096;
+    const bool mine = (lane >> 4) == rank;  // this lane's word of an own row is of this CTA's dims
     bool more = false;
     auto fetch = [&](int t) {  // tile t's descriptor, and its words on their way
       const int ring = t % kInfo;
@@ -384,20 +380,35 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
       const TileInfo& x = infos[ring];
       more = !(x.flags & kEnd);
       if (more) {
-        const uint32_t m = x.mask[rank] >> r0;
-        const uint8_t* base = a.cache;  // dense: the first of the four rows
-        if constexpr (!SPARSE) base += x.at[2 * rank + (w >> 2)] + (r0 & 15) * kLatentRowFp8;
+        const uint32_t m = x.mask[rank] >> r0, mf = x.mask[1 - rank] >> r0;
+        const uint8_t *base = a.cache, *fbase = a.cache;  // dense: the first of the four rows
+        if constexpr (!SPARSE) {
+          base += x.at[2 * rank + (w >> 2)] + (r0 & 15) * kLatentRowFp8;
+          fbase += x.at[2 - 2 * rank + (w >> 2)] + (r0 & 15) * kLatentRowFp8;
+        }
         auto row_of = [&](int j) -> const uint8_t* {
           if constexpr (SPARSE) return a.cache + places[ring * kT + 32 * rank + r0 + j];
           else return base + j * kLatentRowFp8;
         };
-        nxt.scale = 1.f;
+        auto far_of = [&](int j) -> const uint8_t* {
+          if constexpr (SPARSE) return a.cache + places[ring * kT + 32 - 32 * rank + r0 + j];
+          else return fbase + j * kLatentRowFp8;
+        };
+        nxt.scale = nxt.far_scale = 1.f;
         nxt.rot = make_uint4(0, 0, 0, 0);
         if (lane < 16 && ((m >> (lane >> 2)) & 1u)) nxt.scale = ld_nc_f(row_of(lane >> 2) + 512 + (lane & 3) * 4);
+        if (lane < 8 && ((mf >> (lane >> 1)) & 1u))
+          nxt.far_scale = ld_nc_f(far_of(lane >> 1) + 512 + (2 * rank + (lane & 1)) * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           nxt.code[j] = make_uint4(0, 0, 0, 0);
           if ((m >> j) & 1u) nxt.code[j] = ld_nc_v4(row_of(j) + lane * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = 2 * i + (lane >> 4);
+          nxt.far[i] = make_uint4(0, 0, 0, 0);
+          if ((mf >> j) & 1u) nxt.far[i] = ld_nc_v4(far_of(j) + rank * 256 + (lane & 15) * 16);
         }
         if ((m >> (lane >> 3)) & 1u) nxt.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
       }
@@ -410,6 +421,8 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
       const int ring = t & 1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) use_now(nxt.code[j]);  // the tile's words have arrived
+      use_now(nxt.far[0]);
+      use_now(nxt.far[1]);
       use_now(nxt.rot);
       cur = nxt;
       ok = fetch(t + 1);
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) e4m3x16_to_bf16x16(cur.code[j], f[j], o[j]);
       if (t >= 2) {
-        ok = wait(&s_full[ring], ((t >> 1) - 1) & 1);  // the keys of tile t - 2 have been read, in both CTAs
+        ok = wait(&s_full[ring], ((t >> 1) - 1) & 1);  // the keys of tile t - 2 have been read
         if (!ok) break;
       }
       st_shared_v4(smem_u32(ks) + ring * kKBytes + 8 * 4096 + sw128_offset(r0 + (lane >> 3), lane & 7), cur.rot);
@@ -438,17 +451,27 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
         ok = wait(&pv_done[ring], ((t >> 1) - 1) & 1);  // and its values
         if (!ok) break;
       }
+      const uint32_t dst = vto + ring * kVBytes;
+      if (mine) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 lo = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]), hi = make_uint4(o[j][4], o[j][5], o[j][6], o[j][7]);
-        const uint32_t dst = vto + ring * kVBytes;
-        st_cluster_v4(dst + sw128_offset(32 * rank + r0 + j, 2 * wch + odd), odd ? hi : lo);
-        st_cluster_v4(dst + sw128_offset(32 * rank + r0 + j, 2 * wch + 1 - odd), odd ? lo : hi);
+        for (int j = 0; j < 4; ++j) {
+          const uint4 lo = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]), hi = make_uint4(o[j][4], o[j][5], o[j][6], o[j][7]);
+          st_shared_v4(dst + sw128_offset(32 * rank + r0 + j, 2 * wch + odd), odd ? hi : lo);
+          st_shared_v4(dst + sw128_offset(32 * rank + r0 + j, 2 * wch + 1 - odd), odd ? lo : hi);
+        }
       }
-      fence_proxy_async_pair();
       __syncwarp();
-      if (lane == 0) arrive_cluster_release(dsmem_addr(&v_full[ring], 0));
-      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = 2 * i + (lane >> 4);
+        e4m3x16_to_bf16x16(cur.far[i], __shfl_sync(0xffffffffu, cur.far_scale, 2 * j + ((lane >> 3) & 1)), o[i]);
+        const uint4 lo = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]), hi = make_uint4(o[i][4], o[i][5], o[i][6], o[i][7]);
+        const int row = 32 - 32 * rank + r0 + j;
+        st_shared_v4(dst + sw128_offset(row, 2 * wch + odd), odd ? hi : lo);
+        st_shared_v4(dst + sw128_offset(row, 2 * wch + 1 - odd), odd ? lo : hi);
+      }
+      fence_proxy_async_smem();
+      tell_first(&v_full[ring]);
     }
   }
 
