@@ -479,20 +479,25 @@ IC_DEV uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-// Sixteen e4m3 codes times a scale as bf16 (eight packed pairs, lowest byte
-// first). Exact where the scale is a power of two; otherwise each product is
-// rounded to bf16.
+// e4m3 codes times a scale as bf16 (packed pairs, lowest byte first). Exact
+// where the scale is a power of two; otherwise each product is rounded to bf16.
+IC_DEV void e4m3x4_to_bf16x4(uint32_t c, float scale, uint32_t& o0, uint32_t& o1) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(c, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  o0 = pack_bf16x2(a.x * scale, a.y * scale);
+  o1 = pack_bf16x2(b.x * scale, b.y * scale);
+}
+IC_DEV void e4m3x8_to_bf16x8(const uint2& c, float scale, uint32_t (&o)[4]) {
+  e4m3x4_to_bf16x4(c.x, scale, o[0], o[1]);
+  e4m3x4_to_bf16x4(c.y, scale, o[2], o[3]);
+}
 IC_DEV void e4m3x16_to_bf16x16(const uint4& c, float scale, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t lo, hi;
-    e4m3x4_to_f16x4(w[i], lo, hi);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    o[2 * i] = pack_bf16x2(a.x * scale, a.y * scale);
-    o[2 * i + 1] = pack_bf16x2(b.x * scale, b.y * scale);
-  }
+  e4m3x4_to_bf16x4(c.x, scale, o[0], o[1]);
+  e4m3x4_to_bf16x4(c.y, scale, o[2], o[3]);
+  e4m3x4_to_bf16x4(c.z, scale, o[4], o[5]);
+  e4m3x4_to_bf16x4(c.w, scale, o[6], o[7]);
 }
 
 // What was loaded into w is waited for before anything that follows is issued.

@@ -33,11 +33,11 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (t >= a.T) return;
   const int64_t slot = a.slots[t];
-  // this lane's 16 latent values and its rotary pair, requested before the
-  // slot is known
+  // this lane's latent values (dims 8 lane and 256 + 8 lane, eight each) and its
+  // rotary pair, requested before the slot is known
   const uint8_t* src = reinterpret_cast<const uint8_t*>(a.kv) + t * a.kv_stride * 2;
-  const uint4 w0 = *reinterpret_cast<const uint4*>(src + lane * 32);
-  const uint4 w1 = *reinterpret_cast<const uint4*>(src + lane * 32 + 16);
+  const uint4 w[2] = {*reinterpret_cast<const uint4*>(src + lane * 16),
+                      *reinterpret_cast<const uint4*>(src + 512 + lane * 16)};
   uint32_t rot = *reinterpret_cast<const uint32_t*>(
       src + 1024 + 4 * lane);
   if (slot < 0 || slot >= a.num_slots) {
@@ -71,124 +71,147 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
   }
   *reinterpret_cast<uint32_t*>(rdst + 4 * lane) = rot;
   if constexpr (!FP8) {
-    *reinterpret_cast<uint4*>(dst + lane * 32) = w0;
-    *reinterpret_cast<uint4*>(dst + lane * 32 + 16) = w1;
+    *reinterpret_cast<uint4*>(dst + lane * 16) = w[0];
+    *reinterpret_cast<uint4*>(dst + 512 + lane * 16) = w[1];
   } else {
-    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    // largest finite |y| of the 128 dims (8 lanes)
-    float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float x = fabsf(bf16_lane(w[i >> 1], i & 1));
-      if (x < INFINITY) amax = fmaxf(amax, x);
-    }
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      // largest finite |y| of the 128 dims (16 lanes)
+      float amax = 0.f;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // amax = m 2^E with m in [1, 2); 448 = 1.75 2^8: the least e with
-    // 2^e >= amax / 448 is E - 8, or E - 7 where m > 1.75
-    int e = 0;
-    if (amax > 0.f) {
-      const uint32_t bits = __float_as_uint(amax);  // a bf16 subnormal (E = -127 here) ends at e = -100 all the same
-      e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-      e = e < -100 ? -100 : e;
-    }
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, -e in [-119, 100]
-    uint32_t c[4];
+      for (int i = 0; i < 8; ++i) {
+        const float x = fabsf(bf16_lane(v[i >> 1], i & 1));
+        if (x < INFINITY) amax = fmaxf(amax, x);
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p0 = make_float2(bf16_lane(w[2 * i], 0) * inv, bf16_lane(w[2 * i], 1) * inv);
-      const float2 p1 = make_float2(bf16_lane(w[2 * i + 1], 0) * inv, bf16_lane(w[2 * i + 1], 1) * inv);
-      c[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p0, __NV_SATFINITE, __NV_E4M3)) |
-             (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p1, __NV_SATFINITE, __NV_E4M3)) << 16);
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      // amax = m 2^E with m in [1, 2); 448 = 1.75 2^8: the least e with
+      // 2^e >= amax / 448 is E - 8, or E - 7 where m > 1.75
+      int e = 0;
+      if (amax > 0.f) {
+        const uint32_t bits = __float_as_uint(amax);  // a bf16 subnormal (E = -127 here) ends at e = -100 all the same
+        e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = e < -100 ? -100 : e;
+      }
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, -e in [-119, 100]
+      uint32_t c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 p0 = make_float2(bf16_lane(v[2 * i], 0) * inv, bf16_lane(v[2 * i], 1) * inv);
+        const float2 p1 = make_float2(bf16_lane(v[2 * i + 1], 0) * inv, bf16_lane(v[2 * i + 1], 1) * inv);
+        c[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p0, __NV_SATFINITE, __NV_E4M3)) |
+               (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p1, __NV_SATFINITE, __NV_E4M3)) << 16);
+      }
+      *reinterpret_cast<uint2*>(dst + k * 256 + lane * 8) = make_uint2(c[0], c[1]);
+      if ((lane & 15) == 0)
+        *reinterpret_cast<float*>(dst + 512 + (2 * k + (lane >> 4)) * 4) = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     }
-    *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-    if ((lane & 7) == 0)
-      *reinterpret_cast<float*>(dst + 512 + (lane >> 3) * 4) = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   }
 }
 
-// Output row r belongs to sequence b with cu[b] <= r < cu[b + 1]. A CTA takes
-// kRows consecutive rows, its warps kRows / kWarps each.
-constexpr int kRowsPerWarp = 4;
+// Output row r belongs to sequence b with cu[b] <= r < cu[b + 1]. A warp takes
+// kRowsPerWarp consecutive rows; lane j < kRowsPerWarp finds the place of row j,
+// so that the lookups of a warp are one chain: the sequence (32 probes a step),
+// the page, the rows.
+constexpr int kRowsPerWarp = 8;
+constexpr int kBatch = 4;  // rows in flight
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsPerWarp;
   int64_t end = a.cu[a.B];
+  // the last b with cu[b] <= r0 lies in [lo, lo + n)
+  int lo = 0, n = a.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && a.cu[at] <= r0;
+    const uint32_t m = __ballot_sync(0xffffffffu, below) | 1u;
+    const int last = 31 - __clz(m);
+    n = n - last * step < step ? n - last * step : step;
+    lo += last * step;
+  }
   if (end > a.R) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_status(a.status, IC_ERR_BAD_INDEX);
     end = a.R;
   }
   if (r0 >= end) return;
-  // the last b with cu[b] <= r0
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu[mid] <= r0) lo = mid; else hi = mid - 1;
-  }
-  int b = lo;
-  const uint8_t* src[kRowsPerWarp];
-#pragma unroll
-  for (int j = 0; j < kRowsPerWarp; ++j) {
-    const int64_t r = r0 + j;
-    src[j] = nullptr;
-    if (r < end) {
-      while (b + 1 < a.B && a.cu[b + 1] <= r) ++b;
-      const int64_t p = r - a.cu[b];
+  int64_t from = -1;  // lane j: byte offset of row j
+  if (lane < kRowsPerWarp && r0 + lane < end) {
+    int b = lo;
+    const int64_t r = r0 + lane;
+    while (b + 1 < a.B && a.cu[b + 1] <= r) ++b;
+    const int64_t p = r - a.cu[b];
+    if (p >= 0 && p < static_cast<int64_t>(a.table_width) * a.page_size) {
       const int64_t pi = p / a.page_size;
-      int page = -1;
-      if (p >= 0 && pi < a.table_width) page = a.table[static_cast<int64_t>(b) * a.table_stride + pi];
+      const int page = a.table[static_cast<int64_t>(b) * a.table_stride + pi];
       if (page >= 0 && page < a.num_pages)
-        src[j] = static_cast<const uint8_t*>(a.cache) + page * a.page_stride +
-                 (p - pi * a.page_size) * (FP8 ? 656 : 1152);
-      else if (lane == 0)
-        record_status(a.status, IC_ERR_BAD_INDEX);
+        from = page * a.page_stride + (p - pi * a.page_size) * (FP8 ? kLatentRowFp8 : kLatentRowBf16);
     }
+    if (from < 0) record_status(a.status, IC_ERR_BAD_INDEX);
   }
-  if constexpr (!FP8) {
-    // 72 words of 16 bytes a row
-    uint4 w[kRowsPerWarp][3];
+#pragma unroll 1
+  for (int j0 = 0; j0 < kRowsPerWarp; j0 += kBatch) {
+    const int64_t rb = r0 + j0;
+    if (rb >= end) return;
+    const uint8_t* src[kBatch];
 #pragma unroll
-    for (int j = 0; j < kRowsPerWarp; ++j)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        w[j][k] = make_uint4(0, 0, 0, 0);
-        if (src[j] && lane + 32 * k < 72) w[j][k] = *reinterpret_cast<const uint4*>(src[j] + (lane + 32 * k) * 16);
-      }
-#pragma unroll
-    for (int j = 0; j < kRowsPerWarp; ++j)
-      if (r0 + j < end) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + (r0 + j) * 576);
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          if (lane + 32 * k < 72) dst[lane + 32 * k] = w[j][k];
-      }
-  } else {
-    uint4 c[kRowsPerWarp];
-    uint32_t rot[kRowsPerWarp];
-    float s[kRowsPerWarp];
-#pragma unroll
-    for (int j = 0; j < kRowsPerWarp; ++j) {
-      c[j] = make_uint4(0, 0, 0, 0);
-      rot[j] = 0;
-      s[j] = 0.f;
-      if (src[j]) {
-        c[j] = *reinterpret_cast<const uint4*>(src[j] + lane * 16);
-        s[j] = *reinterpret_cast<const float*>(src[j] + 512 + (lane >> 3) * 4);
-        rot[j] = *reinterpret_cast<const uint32_t*>(src[j] + 528 + lane * 4);
-      }
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t o = __shfl_sync(0xffffffffu, from, j0 + j);
+      src[j] = o < 0 ? nullptr : static_cast<const uint8_t*>(a.cache) + o;
     }
+    if constexpr (!FP8) {
+      // 72 words of 16 bytes a row
+      uint4 w[kBatch][3];
 #pragma unroll
-    for (int j = 0; j < kRowsPerWarp; ++j)
-      if (r0 + j < end) {
-        uint32_t o[8];
-        e4m3x16_to_bf16x16(c[j], s[j], o);
-        uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + (r0 + j) * 576);
-        *reinterpret_cast<uint4*>(dst + lane * 32) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + lane * 32 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint32_t*>(dst + 1024 + lane * 4) = rot[j];
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          w[j][k] = make_uint4(0, 0, 0, 0);
+          if (src[j] && lane + 32 * k < 72) w[j][k] = *reinterpret_cast<const uint4*>(src[j] + (lane + 32 * k) * 16);
+        }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (rb + j < end) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (rb + j) * 576);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (lane + 32 * k < 72) dst[lane + 32 * k] = w[j][k];
+        }
+    } else {
+      // lane l has dims 8 l and 256 + 8 l, so that each store fills whole lines
+      uint2 c[kBatch][2];
+      uint32_t rot[kBatch];
+      float s[kBatch][2];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        rot[j] = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          c[j][k] = make_uint2(0, 0);
+          s[j][k] = 0.f;
+          if (src[j]) {
+            c[j][k] = *reinterpret_cast<const uint2*>(src[j] + k * 256 + lane * 8);
+            s[j][k] = *reinterpret_cast<const float*>(src[j] + 512 + (2 * k + (lane >> 4)) * 4);
+          }
+        }
+        if (src[j]) rot[j] = *reinterpret_cast<const uint32_t*>(src[j] + 528 + lane * 4);
       }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (rb + j < end) {
+          uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + (rb + j) * 576);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t o[4];
+            e4m3x8_to_bf16x8(c[j][k], s[j][k], o);
+            *reinterpret_cast<uint4*>(dst + k * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          *reinterpret_cast<uint32_t*>(dst + 1024 + lane * 4) = rot[j];
+        }
+    }
   }
 }
 

@@ -83,17 +83,15 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const RopeArgs a, in
   const int nt = a.T - t0 < tpc ? static_cast<int>(a.T - t0) : tpc;
   const int h0 = blockIdx.y * hpc;
   const int nh = a.H - h0 < hpc ? a.H - h0 : hpc;
-  fill_table(a, cs, t0, nt);
-  __syncthreads();
   const int upt = nh * (ru + cu);  // units of one token
   const int units = nt * upt;
   const int pairs = a.rot_dim / 2;
   const T* x = static_cast<const T*>(a.x);
   T* y = static_cast<T*>(a.out);
-  for (int base = threadIdx.x; base < units; base += kThreads * kUnroll) {
-    uint4 w0[kUnroll], w1[kUnroll];
-    int64_t yo[kUnroll];
-    int ci[kUnroll];  // first pair of the unit in cs, or -1 (copied), -2 (none)
+  uint4 w0[kUnroll], w1[kUnroll];
+  int64_t yo[kUnroll];
+  int ci[kUnroll];  // first pair of the unit in cs, or -1 (copied), -2 (none)
+  auto load = [&](int base) {
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       const int u = base + j * kThreads;
@@ -118,6 +116,12 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const RopeArgs a, in
         if (HALF && ci[j] >= 0) w1[j] = *reinterpret_cast<const uint4*>(x + xo + pairs);
       }
     }
+  };
+  // the first words are on their way while the table is formed
+  load(threadIdx.x);
+  fill_table(a, cs, t0, nt);
+  __syncthreads();
+  for (int base = threadIdx.x;;) {
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       if (ci[j] >= 0) {
@@ -147,6 +151,9 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const RopeArgs a, in
       }
       if (ci[j] >= -1) *reinterpret_cast<uint4*>(y + yo[j]) = w0[j];
     }
+    base += kThreads * kUnroll;
+    if (base >= units) break;
+    load(base);
   }
 }
 
@@ -196,8 +203,13 @@ cudaError_t launch_t(const RopeArgs& a, bool vec, cudaStream_t stream) {
   int tpc = want / (hpc * per_head);
   const int most = 4096 / (a.rot_dim / 2);  // 32 KB of table
   if (tpc > most) tpc = most;
-  // few tokens: one a CTA, so that their loads spread over the SMs
+  // few tokens: one a CTA, so that their loads spread over the SMs; many: up to
+  // four times the work, so that the table's latency (a 64-bit product and a
+  // sine) is paid less often
   while (tpc > 1 && (a.T + tpc - 1) / tpc < 296) tpc /= 2;
+  if (tpc < 1) tpc = 1;
+  const int heads = (a.H + hpc - 1) / hpc;
+  for (int i = 0; i < 2 && 2 * tpc <= most && (a.T + 2 * tpc - 1) / (2 * tpc) * heads >= 1184; ++i) tpc *= 2;
   if (tpc < 1) tpc = 1;
   const int64_t gx = (a.T + tpc - 1) / tpc;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((a.H + hpc - 1) / hpc));

@@ -329,6 +329,8 @@ def reuse_overlap(layers: Sequence, schedule: str, topk: int, n_valid: Optional[
 LATENT_ROW_BYTES = 656  # an e4m3 row of the paged latent cache
 _ROPE_LAYOUT = {"interleaved": _abi.IC_ROPE_INTERLEAVED, "half": _abi.IC_ROPE_HALF}
 _ROPE_DTYPE = _OUT_DTYPE = {torch.bfloat16: _abi.IC_BF16, torch.float32: _abi.IC_F32}
+_CACHE_FORM = "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8"
+_ROT_SHAPE = ((D_QK - D_V) // 2,)
 _SM_SCALE = 1.0 / math.sqrt(D_QK)
 
 
@@ -425,18 +427,23 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, rot_off: int = 
             return rope(x, pos, freq, rot_off, layout, mscale, transpose, out)
     dev = x.get_device()
     _same_device(dev, pos, freq, out)
-    _need(x.dim() == 3 and x.dtype in _ROPE_DTYPE, "x is [T, H, D], bf16 or fp32")
+    if x.dim() != 3 or x.dtype not in _ROPE_DTYPE:
+        raise ValueError("x is [T, H, D], bf16 or fp32")
     T, H, D = x.shape
     xt, xh, xd = x.stride()
     rot = 2 * freq.numel()
-    _need(xd == 1 or D == 1, "x is dense along D")
-    _need(pos.shape == (T,) and pos.dtype == torch.int64, "pos is int64 [T]")
-    _need(freq.dim() == 1 and freq.dtype == torch.float64, "freq is float64 [rot_dim / 2]")
-    _need(layout in _ROPE_LAYOUT, "layout is interleaved or half")
-    _need(0 <= rot_off and rot_off + rot <= D, "the rotated dims lie in the head")
-    _need_dense(pos, freq)
+    if xd != 1 and D != 1:
+        raise ValueError("x is dense along D")
+    if pos.shape != (T,) or pos.dtype != torch.int64 or not pos.is_contiguous():
+        raise ValueError("pos is int64 [T], dense")
+    if freq.dim() != 1 or freq.dtype != torch.float64 or not freq.is_contiguous():
+        raise ValueError("freq is float64 [rot_dim / 2], dense")
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError("layout is interleaved or half")
+    if not 0 <= rot_off <= D - rot:
+        raise ValueError("the rotated dims lie in the head")
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        out = x.new_empty((T, H, D))
         ot, oh = H * D, D
     else:
         _need(out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1, "out is like x, dense along D")
@@ -458,13 +465,15 @@ def new_latent_cache(num_pages: int, page_size: int, fp8: bool = False, device="
 
 def _latent_cache(cache: torch.Tensor):
     """(dtype code, num_pages, page_size, page stride in bytes) of a paged latent cache."""
-    _need(cache.dim() == 3, "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8")
+    if cache.dim() != 3:
+        raise ValueError(_CACHE_FORM)
     P, ps, row = cache.shape
     stride, rs, es = cache.stride()
     fp8 = cache.dtype == torch.uint8
-    _need((fp8 and row == LATENT_ROW_BYTES) or (row == D_QK and cache.dtype == torch.bfloat16),
-          "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8")
-    _need(es == 1 and (rs == row or ps <= 1), "the rows of a page are dense")
+    if not (row == LATENT_ROW_BYTES if fp8 else row == D_QK and cache.dtype == torch.bfloat16):
+        raise ValueError(_CACHE_FORM)
+    if es != 1 or (rs != row and ps > 1):
+        raise ValueError("the rows of a page are dense")
     if P <= 1:
         stride = ps * row
     return (_abi.IC_FP8_E4M3, P, ps, stride) if fp8 else (_abi.IC_BF16, P, ps, 2 * stride)
@@ -482,19 +491,26 @@ def latent_append(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, po
     dev = kv.get_device()
     _same_device(dev, slots, cache, pos, freq, workspace)
     code, P, ps, stride = _latent_cache(cache)
-    _need(kv.dim() == 2 and kv.shape[1] == D_QK and kv.dtype == torch.bfloat16, "kv is bf16 [T, 576]")
-    T = kv.shape[0]
-    _need(kv.stride(1) == 1, "kv is dense along a row")
-    _need(slots.shape == (T,) and slots.dtype == torch.int64, "slots is int64 [T]")
-    _need((pos is None) == (freq is None), "pos and freq come together")
+    if kv.dim() != 2 or kv.dtype != torch.bfloat16:
+        raise ValueError("kv is bf16 [T, 576]")
+    T, row = kv.shape
+    kt, kd = kv.stride()
+    if row != D_QK or kd != 1:
+        raise ValueError("kv is bf16 [T, 576], dense along a row")
+    if slots.shape != (T,) or slots.dtype != torch.int64 or not slots.is_contiguous():
+        raise ValueError("slots is int64 [T], dense")
+    if (pos is None) != (freq is None):
+        raise ValueError("pos and freq come together")
     if pos is not None:
-        _need(pos.shape == (T,) and pos.dtype == torch.int64, "pos is int64 [T]")
-        _need(freq.shape == ((D_QK - D_V) // 2,) and freq.dtype == torch.float64, "freq is float64 [32]")
-    _need(layout in _ROPE_LAYOUT, "layout is interleaved or half")
-    _need_dense(slots, pos, freq)
+        if pos.shape != (T,) or pos.dtype != torch.int64 or not pos.is_contiguous():
+            raise ValueError("pos is int64 [T], dense")
+        if freq.shape != _ROT_SHAPE or freq.dtype != torch.float64 or not freq.is_contiguous():
+            raise ValueError("freq is float64 [32], dense")
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError("layout is interleaved or half")
     workspace = _workspace(workspace, _abi.IC_STATUS_BYTES, kv.device)
     if T > 0:
-        _abi.ic_latent_append(kv.data_ptr(), kv.stride(0), slots.data_ptr(), _addr(pos), _addr(freq), mscale,
+        _abi.ic_latent_append(kv.data_ptr(), kt, slots.data_ptr(), _addr(pos), _addr(freq), mscale,
                               _ROPE_LAYOUT[layout], T, code, cache.data_ptr(), P, ps, stride, workspace.data_ptr(),
                               workspace.numel(), _current_stream(dev))
     return workspace
@@ -526,32 +542,39 @@ def latent_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
 
 def _block_table(table: torch.Tensor):
     """(rows, width, row stride) of a block table."""
-    _need(table.dim() == 2 and table.dtype == torch.int32, "block_table is int32 [B, width]")
+    if table.dim() != 2 or table.dtype != torch.int32:
+        raise ValueError("block_table is int32 [B, width]")
     B, width = table.shape
     stride, one = table.stride()
     if B <= 1:
         stride = width
-    _need((one == 1 or width <= 1) and stride >= width, "block_table is dense along a row")
+    if (one != 1 and width > 1) or stride < width:
+        raise ValueError("block_table is dense along a row")
     return B, width, stride
 
 
 def _attention_args(q, sink, gate, out, out_dtype, lse, want_lse):
     """Checks the arguments that the two attentions share; makes the outputs that are not given."""
-    lead = q.shape[:-1]
+    shape = q.shape
+    lead = shape[:-1]
     wide = lead + (D_V,)
-    _need(q.shape[-1] == D_QK and q.dtype == torch.bfloat16, "q is bf16 [..., H, 576]")
-    _need(sink is None or (sink.shape == lead[-1:] and sink.dtype == torch.float32), "sink is fp32 [H]")
-    _need(gate is None or (gate.shape == wide and gate.dtype == torch.bfloat16), "gate is bf16 [..., H, 512]")
-    _need_dense(q, sink, gate, out, lse)
+    if shape[-1] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q is bf16 [..., H, 576], dense")
+    if sink is not None and (sink.shape != lead[-1:] or sink.dtype != torch.float32 or not sink.is_contiguous()):
+        raise ValueError("sink is fp32 [H], dense")
+    if gate is not None and (gate.shape != wide or gate.dtype != torch.bfloat16 or not gate.is_contiguous()):
+        raise ValueError("gate is bf16 [..., H, 512], dense")
     if out is None:
-        _need(out_dtype in _OUT_DTYPE, "out is bf16 or fp32")
-        out = torch.empty(wide, dtype=out_dtype, device=q.device)
-    else:
-        _need(out.shape == wide and out.dtype in _OUT_DTYPE, "out is [..., H, 512], bf16 or fp32")
+        if out_dtype not in _OUT_DTYPE:
+            raise ValueError("out is bf16 or fp32")
+        out = q.new_empty(wide) if out_dtype == torch.bfloat16 else q.new_empty(wide, dtype=out_dtype)
+    elif out.shape != wide or out.dtype not in _OUT_DTYPE or not out.is_contiguous():
+        raise ValueError("out is [..., H, 512], bf16 or fp32, dense")
     if lse is not None:
-        _need(lse.shape == lead and lse.dtype == torch.float32, "lse is fp32 [..., H]")
+        if lse.shape != lead or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse is fp32 [..., H], dense")
     elif want_lse:
-        lse = torch.empty(lead, dtype=torch.float32, device=q.device)
+        lse = q.new_empty(lead, dtype=torch.float32)
     return out, lse
 
 
@@ -581,10 +604,14 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     _same_device(dev, cache, block_table, lens, sink, gate, out, lse, workspace)
     code, P, ps, stride = _latent_cache(cache)
     TB, width, table_stride = _block_table(block_table)
-    _need(q.dim() in (3, 4), "q is [B, H, 576] or [B, Q, H, 576]")
-    B, H, Q = q.shape[0], q.shape[-2], (q.shape[1] if q.dim() == 4 else 1)
-    _need(TB == B and lens.shape == (B,) and lens.dtype == torch.int64, "block_table is [B, width], lens int64 [B]")
-    _need_dense(lens)
+    if q.dim() == 4:
+        B, Q, H, _ = q.shape
+    elif q.dim() == 3:
+        (B, H, _), Q = q.shape, 1
+    else:
+        raise ValueError("q is [B, H, 576] or [B, Q, H, 576]")
+    if TB != B or lens.shape != (B,) or lens.dtype != torch.int64 or not lens.is_contiguous():
+        raise ValueError("block_table is [B, width], lens int64 [B], dense")
     out, lse = _attention_args(q, sink, gate, out, out_dtype, lse, want_lse)
     if B > 0 and Q > 0 and H > 0:
         if workspace is None:
