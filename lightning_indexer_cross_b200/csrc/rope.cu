@@ -72,87 +72,111 @@ IC_DEV void fill_table(const RopeArgs& a, float2* cs, int64_t t0, int nt) {
   }
 }
 
-// 16-byte words. Units of one head: `ru` rotated ones (interleaved: one word
-// of N / 2 pairs; half: a word of the first half and its partner), then `cu`
-// words that are copied (none when the rotation is in place).
+// i / d for i d < 2^32, with m = 2^32 / d + 1 from the host: a word's work is
+// otherwise half index arithmetic.
+struct Div {
+  uint32_t d, m;
+};
+Div make_div(uint32_t d) { return Div{d, d > 1 ? static_cast<uint32_t>((uint64_t(1) << 32) / d + 1) : 0}; }
+IC_DEV uint32_t quot(uint32_t i, const Div& v) { return v.d == 1 ? i : __umulhi(i, v.m); }
+
+// 16-byte words. Units of one (token, head) row: `ru` rotated ones (interleaved:
+// one word of N / 2 pairs; half: a word of the first half and its partner), and
+// `cu` words that are copied (none when the rotation is in place). The first
+// rotated words are on their way, and the copies done, before the table is
+// needed.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const RopeArgs a, int tpc, int hpc, int ru, int cu) {
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const RopeArgs a, int tpc, int hpc, const Div ru, const Div cu,
+                                                            const Div nh_full, const Div nh_last) {
   constexpr int N = Vec<T>::N;
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float2 cs[];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpc;
   const int nt = a.T - t0 < tpc ? static_cast<int>(a.T - t0) : tpc;
   const int h0 = blockIdx.y * hpc;
-  const int nh = a.H - h0 < hpc ? a.H - h0 : hpc;
-  const int upt = nh * (ru + cu);  // units of one token
-  const int units = nt * upt;
+  const Div nh = blockIdx.y + 1 == gridDim.y ? nh_last : nh_full;
+  const uint32_t rows = nt * nh.d;
   const int pairs = a.rot_dim / 2;
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.out);
+  const T* x = static_cast<const T*>(a.x) + t0 * a.x_ts + h0 * a.x_hs;
+  T* y = static_cast<T*>(a.out) + t0 * a.y_ts + h0 * a.y_hs;
+  const uint32_t nr = rows * ru.d, nc = rows * cu.d;
   uint4 w0[kUnroll], w1[kUnroll];
-  int64_t yo[kUnroll];
-  int ci[kUnroll];  // first pair of the unit in cs, or -1 (copied), -2 (none)
-  auto load = [&](int base) {
+  auto load = [&](uint32_t base) {
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      const int u = base + j * kThreads;
-      ci[j] = -2;
-      if (u < units) {
-        const int t = u / upt, r = u - t * upt;
-        const int h = r / (ru + cu), e = r - h * (ru + cu);
-        int64_t xo = (t0 + t) * a.x_ts + static_cast<int64_t>(h0 + h) * a.x_hs;
-        yo[j] = (t0 + t) * a.y_ts + static_cast<int64_t>(h0 + h) * a.y_hs;
-        int d;
-        if (e < ru) {
-          d = a.rot_off + e * N;
-          ci[j] = t * pairs + (HALF ? e * N : e * (N / 2));
-        } else {
-          d = (e - ru) * N;
-          if (d >= a.rot_off) d += a.rot_dim;
-          ci[j] = -1;
-        }
-        xo += d;
-        yo[j] += d;
-        w0[j] = *reinterpret_cast<const uint4*>(x + xo);
-        if (HALF && ci[j] >= 0) w1[j] = *reinterpret_cast<const uint4*>(x + xo + pairs);
+      const uint32_t u = base + j * kThreads;
+      if (u < nr) {
+        const uint32_t row = quot(u, ru), e = u - row * ru.d, t = quot(row, nh), h = row - t * nh.d;
+        const T* src = x + t * a.x_ts + h * a.x_hs + a.rot_off + e * N;
+        w0[j] = *reinterpret_cast<const uint4*>(src);
+        if (HALF) w1[j] = *reinterpret_cast<const uint4*>(src + pairs);
       }
     }
   };
-  // the first words are on their way while the table is formed
   load(threadIdx.x);
-  fill_table(a, cs, t0, nt);
-  __syncthreads();
-  for (int base = threadIdx.x;;) {
+  for (uint32_t base = threadIdx.x; base < nc; base += kThreads * kUnroll) {
+    uint4 w[kUnroll];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      if (ci[j] >= 0) {
-        float u[N];
-        Vec<T>::unpack(w0[j], u);
-        if constexpr (HALF) {
-          float v[N];
-          Vec<T>::unpack(w1[j], v);
+      const uint32_t u = base + j * kThreads;
+      if (u < nc) {
+        const uint32_t row = quot(u, cu), t = quot(row, nh), h = row - t * nh.d;
+        int d = (u - row * cu.d) * N;
+        if (d >= a.rot_off) d += a.rot_dim;
+        w[j] = *reinterpret_cast<const uint4*>(x + t * a.x_ts + h * a.x_hs + d);
+      }
+    }
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float2 r = cs[ci[j] + i];
-            const float p = u[i], q = v[i];
-            u[i] = p * r.x - q * r.y;
-            v[i] = p * r.y + q * r.x;
+    for (int j = 0; j < kUnroll; ++j) {
+      const uint32_t u = base + j * kThreads;
+      if (u < nc) {
+        const uint32_t row = quot(u, cu), t = quot(row, nh), h = row - t * nh.d;
+        int d = (u - row * cu.d) * N;
+        if (d >= a.rot_off) d += a.rot_dim;
+        *reinterpret_cast<uint4*>(y + t * a.y_ts + h * a.y_hs + d) = w[j];
+      }
+    }
+  }
+  fill_table(a, cs, t0, nt);
+  __syncthreads();
+  for (uint32_t base = threadIdx.x;;) {
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const uint32_t u = base + j * kThreads;
+      if (u < nr) {
+        const uint32_t row = quot(u, ru), e = u - row * ru.d, t = quot(row, nh), h = row - t * nh.d;
+        T* dst = y + t * a.y_ts + h * a.y_hs + a.rot_off + e * N;
+        const float4* c4 = reinterpret_cast<const float4*>(cs + t * pairs + e * (HALF ? N : N / 2));  // two pairs each
+        float p[N];
+        Vec<T>::unpack(w0[j], p);
+        if constexpr (HALF) {
+          float q[N];
+          Vec<T>::unpack(w1[j], q);
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const float4 r = c4[i / 2];
+            const float p0 = p[i], q0 = q[i], p1 = p[i + 1], q1 = q[i + 1];
+            p[i] = p0 * r.x - q0 * r.y;
+            q[i] = p0 * r.y + q0 * r.x;
+            p[i + 1] = p1 * r.z - q1 * r.w;
+            q[i + 1] = p1 * r.w + q1 * r.z;
           }
-          *reinterpret_cast<uint4*>(y + yo[j] + pairs) = Vec<T>::pack(v);
+          *reinterpret_cast<uint4*>(dst + pairs) = Vec<T>::pack(q);
         } else {
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            const float2 r = cs[ci[j] + i];
-            const float p = u[2 * i], q = u[2 * i + 1];
-            u[2 * i] = p * r.x - q * r.y;
-            u[2 * i + 1] = p * r.y + q * r.x;
+          for (int i = 0; i < N / 4; ++i) {
+            const float4 r = c4[i];
+            const float p0 = p[4 * i], q0 = p[4 * i + 1], p1 = p[4 * i + 2], q1 = p[4 * i + 3];
+            p[4 * i] = p0 * r.x - q0 * r.y;
+            p[4 * i + 1] = p0 * r.y + q0 * r.x;
+            p[4 * i + 2] = p1 * r.z - q1 * r.w;
+            p[4 * i + 3] = p1 * r.w + q1 * r.z;
           }
         }
-        w0[j] = Vec<T>::pack(u);
+        *reinterpret_cast<uint4*>(dst) = Vec<T>::pack(p);
       }
-      if (ci[j] >= -1) *reinterpret_cast<uint4*>(y + yo[j]) = w0[j];
     }
     base += kThreads * kUnroll;
-    if (base >= units) break;
+    if (base >= nr) break;
     load(base);
   }
 }
@@ -214,12 +238,16 @@ cudaError_t launch_t(const RopeArgs& a, bool vec, cudaStream_t stream) {
   const int64_t gx = (a.T + tpc - 1) / tpc;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((a.H + hpc - 1) / hpc));
   const size_t smem = static_cast<size_t>(tpc) * (a.rot_dim / 2) * sizeof(float2);
-  if (!vec)
+  if (!vec) {
     rope_elem_kernel<T><<<grid, kThreads, smem, stream>>>(a, tpc, hpc, ru, cu);
-  else if (a.half)
-    rope_vec_kernel<T, true><<<grid, kThreads, smem, stream>>>(a, tpc, hpc, ru, cu);
+    return cudaGetLastError();
+  }
+  const Div dr = make_div(ru), dc = make_div(cu > 0 ? cu : 1), nf = make_div(hpc), nl = make_div(a.H - (grid.y - 1) * hpc);
+  const Div copies{cu > 0 ? dc.d : 0, dc.m};
+  if (a.half)
+    rope_vec_kernel<T, true><<<grid, kThreads, smem, stream>>>(a, tpc, hpc, dr, copies, nf, nl);
   else
-    rope_vec_kernel<T, false><<<grid, kThreads, smem, stream>>>(a, tpc, hpc, ru, cu);
+    rope_vec_kernel<T, false><<<grid, kThreads, smem, stream>>>(a, tpc, hpc, dr, copies, nf, nl);
   return cudaGetLastError();
 }
 
