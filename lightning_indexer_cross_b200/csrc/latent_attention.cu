@@ -435,11 +435,14 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
     for (int u = 0; more; ++u) {
       const int t = u >> 1, h = u & 1;
       if (h == 0) {
-        if (kQStage && first) {  // the first of these warps copies Q
+        // Every warp waits for every stage, Q's too, which the first of them
+        // copies: a warp that skipped one could be two phases ahead at its next
+        // wait, and take an older phase of the same parity for its own.
+        if (kQStage && first) {
+          const int qs = n % kStages;
+          ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
+          if (!ok) break;
           if (w == 0) {
-            const int qs = n % kStages;
-            ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
-            if (!ok) break;
             if (lane == 0) {
               mbar_arrive_n(&full[qs], 7);
               mbar_arrive_expect_tx(&full[qs], 9 * R::kQSlab);
@@ -526,8 +529,8 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
   const int row = rest / kCtas * 32 + lane;
   const int dim = (rest % kCtas * kPerCta + warp / WPP) * 16;
   pdl_trigger();
-  pdl_wait();
-  // tiles of all sequences, and of those before b
+  // tiles of all sequences, and of those before b. (The lengths were there before
+  // the main kernel started, so they are read before it ends.)
   int64_t total = 0, start = 0;
   int bt;
   if (SPARSE) {
@@ -569,12 +572,23 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
       gf = static_cast<int>(((start + 1) * G - 1) / total);
       gl = static_cast<int>(((start + bt) * G - 1) / total);
     }
-    if (gf == gl) return;  // one piece: written already
+    if (gf == gl) {  // one piece: written already
+      pdl_wait();    // (no CTA ends before the main kernel, so that the stream's next one cannot start before it)
+      return;
+    }
     // only the first of the groups may hold another sequence before this one
     first_slot = share_start(gf, total, G) < start ? 1 : 0;
   }
   const bool live = row < a.rows;
   const int rb = row / M, r = row % M;
+  const int64_t gr = static_cast<int64_t>(b) * a.rows + row;
+  uint4 gates[2] = {};
+  if (a.gate && live && warp % WPP == 0) {
+    gates[0] = reinterpret_cast<const uint4*>(a.gate + gr * 512 + dim)[0];
+    gates[1] = reinterpret_cast<const uint4*>(a.gate + gr * 512 + dim)[1];
+  }
+  const float sink2 = a.sink && live ? a.sink[row % a.H] * kLog2e : -INFINITY;
+  pdl_wait();
   float m = -INFINITY, den = 0.f;
   float4 acc[4];
 #pragma unroll
@@ -623,12 +637,10 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
     }
   }
   if (!live) return;
-  const float sink2 = a.sink ? a.sink[row % a.H] * kLog2e : -INFINITY;
   const float top = fmaxf(m, sink2);
   const float w = m == -INFINITY ? 0.f : exp2f(m - top);
   den = den * w + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - top));
   const float f = w > 0.f ? w / den : 0.f;
-  const int64_t gr = static_cast<int64_t>(b) * a.rows + row;
   float o[16];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -638,11 +650,9 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
     o[4 * i + 3] = acc[i].w * f;
   }
   if (a.gate) {
-    const uint4* g = reinterpret_cast<const uint4*>(a.gate + gr * 512 + dim);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const uint4 v = g[k];
-      const uint32_t gw[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t gw[4] = {gates[k].x, gates[k].y, gates[k].z, gates[k].w};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         o[8 * k + e] *= __fdividef(1.f, 1.f + ex2_approx(-kLog2e * bf16_lane(gw[e >> 1], e & 1)));

@@ -571,3 +571,27 @@ def test_every_code_and_scale_is_widened(ops, page_gap):
     rows[1, 78] = 0xff
     out = ops.latent_sparse_decode(q, cache, slots)[0]
     assert out[:2].isnan().all() and not out[2:].isnan().any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_a_wait_that_gives_up_is_recorded_and_the_next_call_is_right(ops, fp8, H):
+    """With the wait limit at 0 a wait that is not satisfied at once gives up: the call returns, its status says so, and
+    the next call with the default limit is right. (No GPU fault is involved: the host tells the waits to give up.)"""
+    from lightning_indexer_cross_b200 import _abi
+    g = gen(13)
+    lens = [1500, 0, 700]
+    table, pages = paged(lens, 64, g)
+    cache = random_cache(ops, pages, 64, fp8, g)
+    q, ln = queries((3, 1, H), g), torch.tensor(lens, device="cuda")
+    ws = ops.new_workspace(ops.latent_decode_workspace_size(3, 1, H, table.shape[1] * 64), "cuda")
+    default = _abi.ic_wait_limit_ns()
+    try:
+        _abi.ic_set_wait_limit_ns(0)
+        ops.latent_decode(q, cache, table, ln, workspace=ws)
+    finally:
+        _abi.ic_set_wait_limit_ns(default)
+    assert status_of(ops, ws) == _abi.IC_ERR_TIMEOUT
+    out, lse = ops.latent_decode(q, cache, table, ln, workspace=ws)
+    assert status_of(ops, ws) == 0
+    check_attention(out, lse, L.decode(q, cache, table, lens), max(lens))
