@@ -25,7 +25,6 @@ IC_F32 = 2
 
 IC_ROPE_INTERLEAVED = 0
 IC_ROPE_HALF = 1
-IC_STATUS_BYTES = 256  # workspace of the calls that only keep a status word
 
 # every symbol include/indexcache.h declares
 EXPORTED = [

@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexcache.so")
+FRONT = os.path.join(PKG, "_front.so")
 SOURCES = ["api.cu", "indexer.cu", "topk.cu", "sparse_mla.cu", "topk_noalloc.cu", "append.cu", "gate.cu", "context_parallel.cu", "topk_threshold.cu", "overlap.cu",
            "rope.cu", "latent_cache.cu", "latent_attention.cu", "latent_pair.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -40,9 +42,9 @@ def _deps():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(FRONT):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FRONT))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -73,7 +75,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_front(cc)
     return LIB
+
+
+def build_front(cc: str) -> None:
+    """The tensor front end, a Python extension that links the library (and torch's, which are loaded with torch)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = os.path.join(root, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+    lib = os.path.join(root, "lib")
+    tmp = FRONT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-O2", "-std=c++17", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", include, "-isystem",
+           os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", cuda, os.path.join(CSRC, "front.cpp"), "-o", tmp, "-L", PKG, "-l:libindexcache.so", "-L", lib,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on front.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FRONT)
 
 
 if __name__ == "__main__":

@@ -7,14 +7,15 @@ allocate outputs and workspaces with torch, and pass raw pointers through
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import List, Optional, Sequence
 
 import torch
 
-from . import _abi
+from . import _abi, _front
+
+_front.set_error(_abi.ICError)
 
 D_QK = 576
 D_V = 512
@@ -328,53 +329,24 @@ def reuse_overlap(layers: Sequence, schedule: str, topk: int, n_valid: Optional[
 
 LATENT_ROW_BYTES = 656  # an e4m3 row of the paged latent cache
 _ROPE_LAYOUT = {"interleaved": _abi.IC_ROPE_INTERLEAVED, "half": _abi.IC_ROPE_HALF}
-_ROPE_DTYPE = _OUT_DTYPE = {torch.bfloat16: _abi.IC_BF16, torch.float32: _abi.IC_F32}
-_CACHE_FORM = "the cache is [num_pages, page_size, 576] bf16 or [num_pages, page_size, 656] uint8"
-_ROT_SHAPE = ((D_QK - D_V) // 2,)
+_LAYOUTS = "layout is interleaved or half"
+_OUT_DTYPE = {torch.bfloat16: _abi.IC_BF16, torch.float32: _abi.IC_F32}
 _SM_SCALE = 1.0 / math.sqrt(D_QK)
 
 
-def _elsewhere(x: torch.Tensor, stream) -> bool:
-    """Whether x is on another device than the current one, or a stream is named: the call is then made again inside
-    ``_on``. (The plain case costs no context manager: a decode step's calls take a few microseconds each.)"""
-    _need_cuda(x)
-    return stream is not None or x.get_device() != torch.cuda.current_device()
-
-
 def _on(x: torch.Tensor, stream):
-    """Context that makes x's device and the launch's stream current: outputs and workspaces made inside are that
-    stream's, so neither their zeroing nor their reuse can overtake the launch."""
-    if stream is None:
-        return torch.cuda.device(x.device)
+    """Context that makes the launch's stream current: outputs and workspaces made inside are that stream's, so neither
+    their zeroing nor their reuse can overtake the launch."""
+    _need_cuda(x)
     if stream.device != x.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
     return torch.cuda.stream(stream)
 
 
-def _same_device(dev: int, *ts) -> None:
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _current_stream(dev: int) -> int:
-    """Handle of dev's current stream, without the object around it (3 us of a call)."""
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> torch.Tensor:
-    """The given byte workspace, or a new one of which only the status word is cleared."""
-    if workspace is None:
-        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
-        workspace[:256].zero_()
-        return workspace
-    _need(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous(),
-          "the workspace is a uint8 vector")
-    return workspace
+def _code(table: dict, key, what: str) -> int:
+    if key not in table:
+        raise ValueError(what)
+    return table[key]
 
 
 def _need(cond: bool, what: str) -> None:
@@ -422,37 +394,10 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, rot_off: int = 
     """Rotary positions: x [T, H, D] (bf16 or fp32, innermost dense) with dims [rot_off, rot_off + 2 len(freq)) of
     every head rotated to pos [T] (int64); the other dims are copied. layout: "interleaved" pairs (2i, 2i + 1) or
     "half" pairs (i, i + len(freq)). transpose=True applies the transposed map (the gradient's). out may be x."""
-    if _elsewhere(x, stream):
+    if stream is not None:
         with _on(x, stream):
             return rope(x, pos, freq, rot_off, layout, mscale, transpose, out)
-    dev = x.get_device()
-    _same_device(dev, pos, freq, out)
-    if x.dim() != 3 or x.dtype not in _ROPE_DTYPE:
-        raise ValueError("x is [T, H, D], bf16 or fp32")
-    T, H, D = x.shape
-    xt, xh, xd = x.stride()
-    rot = 2 * freq.numel()
-    if xd != 1 and D != 1:
-        raise ValueError("x is dense along D")
-    if pos.shape != (T,) or pos.dtype != torch.int64 or not pos.is_contiguous():
-        raise ValueError("pos is int64 [T], dense")
-    if freq.dim() != 1 or freq.dtype != torch.float64 or not freq.is_contiguous():
-        raise ValueError("freq is float64 [rot_dim / 2], dense")
-    if layout not in _ROPE_LAYOUT:
-        raise ValueError("layout is interleaved or half")
-    if not 0 <= rot_off <= D - rot:
-        raise ValueError("the rotated dims lie in the head")
-    if out is None:
-        out = x.new_empty((T, H, D))
-        ot, oh = H * D, D
-    else:
-        _need(out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1, "out is like x, dense along D")
-        ot, oh = out.stride(0), out.stride(1)
-    if T > 0 and H > 0:
-        _abi.ic_rope(x.data_ptr(), xt, xh, pos.data_ptr(), freq.data_ptr(), mscale, _ROPE_LAYOUT[layout],
-                     1 if transpose else 0, _ROPE_DTYPE[x.dtype], T, H, D, rot_off, rot, out.data_ptr(), ot, oh,
-                     _current_stream(dev))
-    return out
+    return _front.rope(x, pos, freq, rot_off, _code(_ROPE_LAYOUT, layout, _LAYOUTS), mscale, transpose, out)
 
 
 def new_latent_cache(num_pages: int, page_size: int, fp8: bool = False, device="cuda") -> torch.Tensor:
@@ -463,57 +408,16 @@ def new_latent_cache(num_pages: int, page_size: int, fp8: bool = False, device="
     return torch.zeros((num_pages, page_size, D_QK), dtype=torch.bfloat16, device=device)
 
 
-def _latent_cache(cache: torch.Tensor):
-    """(dtype code, num_pages, page_size, page stride in bytes) of a paged latent cache."""
-    if cache.dim() != 3:
-        raise ValueError(_CACHE_FORM)
-    P, ps, row = cache.shape
-    stride, rs, es = cache.stride()
-    fp8 = cache.dtype == torch.uint8
-    if not (row == LATENT_ROW_BYTES if fp8 else row == D_QK and cache.dtype == torch.bfloat16):
-        raise ValueError(_CACHE_FORM)
-    if es != 1 or (rs != row and ps > 1):
-        raise ValueError("the rows of a page are dense")
-    if P <= 1:
-        stride = ps * row
-    return (_abi.IC_FP8_E4M3, P, ps, stride) if fp8 else (_abi.IC_BF16, P, ps, 2 * stride)
-
-
 def latent_append(kv: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, pos: Optional[torch.Tensor] = None,
                   freq: Optional[torch.Tensor] = None, layout: str = "interleaved", mscale: float = 1.0,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Write T latent rows kv [T, 576] bf16 into slots[t] (int64, -1 skips; slot = page * page_size + row) of the
     paged cache, quantised if it holds e4m3 rows; with pos [T] and freq [32] the 64 rotary dims are rotated as by
     ``rope``. Returns the workspace (its status word records slots outside the cache)."""
-    if _elsewhere(kv, stream):
+    if stream is not None:
         with _on(kv, stream):
             return latent_append(kv, slots, cache, pos, freq, layout, mscale, workspace)
-    dev = kv.get_device()
-    _same_device(dev, slots, cache, pos, freq, workspace)
-    code, P, ps, stride = _latent_cache(cache)
-    if kv.dim() != 2 or kv.dtype != torch.bfloat16:
-        raise ValueError("kv is bf16 [T, 576]")
-    T, row = kv.shape
-    kt, kd = kv.stride()
-    if row != D_QK or kd != 1:
-        raise ValueError("kv is bf16 [T, 576], dense along a row")
-    if slots.shape != (T,) or slots.dtype != torch.int64 or not slots.is_contiguous():
-        raise ValueError("slots is int64 [T], dense")
-    if (pos is None) != (freq is None):
-        raise ValueError("pos and freq come together")
-    if pos is not None:
-        if pos.shape != (T,) or pos.dtype != torch.int64 or not pos.is_contiguous():
-            raise ValueError("pos is int64 [T], dense")
-        if freq.shape != _ROT_SHAPE or freq.dtype != torch.float64 or not freq.is_contiguous():
-            raise ValueError("freq is float64 [32], dense")
-    if layout not in _ROPE_LAYOUT:
-        raise ValueError("layout is interleaved or half")
-    workspace = _workspace(workspace, _abi.IC_STATUS_BYTES, kv.device)
-    if T > 0:
-        _abi.ic_latent_append(kv.data_ptr(), kt, slots.data_ptr(), _addr(pos), _addr(freq), mscale,
-                              _ROPE_LAYOUT[layout], T, code, cache.data_ptr(), P, ps, stride, workspace.data_ptr(),
-                              workspace.numel(), _current_stream(dev))
-    return workspace
+    return _front.latent_append(kv, slots, cache, pos, freq, _code(_ROPE_LAYOUT, layout, _LAYOUTS), mscale, workspace)
 
 
 def latent_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Tensor, out: torch.Tensor,
@@ -521,61 +425,10 @@ def latent_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
     """Copy sequences out of the paged cache: rows cu_len[b] .. cu_len[b + 1] of out [R, 576] bf16 become the first
     rows of sequence b, found through block_table [B, width] int32; cu_len int64 [B + 1]. Rows behind cu_len[B] are
     left as they are."""
-    if _elsewhere(cache, stream):
+    if stream is not None:
         with _on(cache, stream):
             return latent_read(cache, block_table, cu_len, out, workspace)
-    dev = cache.get_device()
-    _same_device(dev, block_table, cu_len, out, workspace)
-    code, P, ps, stride = _latent_cache(cache)
-    B, width, table_stride = _block_table(block_table)
-    _need(cu_len.shape == (B + 1,) and cu_len.dtype == torch.int64, "cu_len is int64 [B + 1]")
-    _need(out.dim() == 2 and out.shape[1] == D_QK and out.dtype == torch.bfloat16, "out is bf16 [R, 576]")
-    _need_dense(cu_len, out)
-    R = out.shape[0]
-    if R > 0:
-        workspace = _workspace(workspace, _abi.IC_STATUS_BYTES, cache.device)
-        _abi.ic_latent_read(cache.data_ptr(), code, P, ps, stride, block_table.data_ptr(), table_stride, width,
-                            cu_len.data_ptr(), B, out.data_ptr(), R, workspace.data_ptr(), workspace.numel(),
-                            _current_stream(dev))
-    return out
-
-
-def _block_table(table: torch.Tensor):
-    """(rows, width, row stride) of a block table."""
-    if table.dim() != 2 or table.dtype != torch.int32:
-        raise ValueError("block_table is int32 [B, width]")
-    B, width = table.shape
-    stride, one = table.stride()
-    if B <= 1:
-        stride = width
-    if (one != 1 and width > 1) or stride < width:
-        raise ValueError("block_table is dense along a row")
-    return B, width, stride
-
-
-def _attention_args(q, sink, gate, out, out_dtype, lse, want_lse):
-    """Checks the arguments that the two attentions share; makes the outputs that are not given."""
-    shape = q.shape
-    lead = shape[:-1]
-    wide = lead + (D_V,)
-    if shape[-1] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
-        raise ValueError("q is bf16 [..., H, 576], dense")
-    if sink is not None and (sink.shape != lead[-1:] or sink.dtype != torch.float32 or not sink.is_contiguous()):
-        raise ValueError("sink is fp32 [H], dense")
-    if gate is not None and (gate.shape != wide or gate.dtype != torch.bfloat16 or not gate.is_contiguous()):
-        raise ValueError("gate is bf16 [..., H, 512], dense")
-    if out is None:
-        if out_dtype not in _OUT_DTYPE:
-            raise ValueError("out is bf16 or fp32")
-        out = q.new_empty(wide) if out_dtype == torch.bfloat16 else q.new_empty(wide, dtype=out_dtype)
-    elif out.shape != wide or out.dtype not in _OUT_DTYPE or not out.is_contiguous():
-        raise ValueError("out is [..., H, 512], bf16 or fp32, dense")
-    if lse is not None:
-        if lse.shape != lead or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError("lse is fp32 [..., H], dense")
-    elif want_lse:
-        lse = q.new_empty(lead, dtype=torch.float32)
-    return out, lse
+    return _front.latent_read(cache, block_table, cu_len, out, workspace)
 
 
 def latent_decode_workspace_size(B: int, Q: int, H: int, max_len: int) -> int:
@@ -596,34 +449,12 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     """Dense latent attention over the paged cache: q [B, H, 576] (one new token a sequence) or [B, Q, H, 576] (Q new
     tokens, token j seeing lens[b] - (Q - 1 - j) rows), block_table [B, width] int32, lens [B] int64 (0: an idle
     slot). Returns (out [..., H, 512], lse [..., H])."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on(q, stream):
             return latent_decode(q, cache, block_table, lens, sink, gate, sm_scale, out_dtype, out, lse, want_lse,
                                  workspace)
-    dev = q.get_device()
-    _same_device(dev, cache, block_table, lens, sink, gate, out, lse, workspace)
-    code, P, ps, stride = _latent_cache(cache)
-    TB, width, table_stride = _block_table(block_table)
-    if q.dim() == 4:
-        B, Q, H, _ = q.shape
-    elif q.dim() == 3:
-        (B, H, _), Q = q.shape, 1
-    else:
-        raise ValueError("q is [B, H, 576] or [B, Q, H, 576]")
-    if TB != B or lens.shape != (B,) or lens.dtype != torch.int64 or not lens.is_contiguous():
-        raise ValueError("block_table is [B, width], lens int64 [B], dense")
-    out, lse = _attention_args(q, sink, gate, out, out_dtype, lse, want_lse)
-    if B > 0 and Q > 0 and H > 0:
-        if workspace is None:
-            workspace = _workspace(None, _abi.ic_latent_decode_workspace_size(B, Q, H, width * ps), q.device)
-        else:
-            _workspace(workspace, 0, q.device)
-        _abi.ic_latent_decode(q.data_ptr(), cache.data_ptr(), code, P, ps, stride, block_table.data_ptr(),
-                              table_stride, width, lens.data_ptr(), _addr(sink), _addr(gate),
-                              _SM_SCALE if sm_scale is None else sm_scale, B, Q, H, _OUT_DTYPE[out.dtype],
-                              out.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel(),
-                              _current_stream(dev))
-    return out, lse
+    return _front.latent_decode(q, cache, block_table, lens, sink, gate, _SM_SCALE if sm_scale is None else sm_scale,
+                                _code(_OUT_DTYPE, out_dtype, "out is bf16 or fp32"), out, lse, want_lse, workspace)
 
 
 def latent_sparse_decode(q: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
@@ -634,30 +465,12 @@ def latent_sparse_decode(q: torch.Tensor, cache: torch.Tensor, slots: torch.Tens
     """``sparse_mla_decode`` over an e4m3 paged cache: q [B, H, 576] attends to slots [B, k] (int32, -1 padding) of
     the cache. Returns (out [B, H, 512], lse [B, H]). (Dense bf16 pages: ``sparse_mla_decode`` with
     cache.view(1, -1, 576) and the slots as idx.)"""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on(q, stream):
-            return latent_sparse_decode(q, cache, slots, sink, gate, sm_scale, out_dtype, out, lse, want_lse,
-                                        workspace)
-    dev = q.get_device()
-    _same_device(dev, cache, slots, sink, gate, out, lse, workspace)
-    code, P, ps, stride = _latent_cache(cache)
-    _need(code == _abi.IC_FP8_E4M3, "the cache holds e4m3 rows")
-    _need(q.dim() == 3, "q is [B, H, 576]")
-    B, H, _ = q.shape
-    _need(slots.dim() == 2 and slots.shape[0] == B and slots.dtype == torch.int32, "slots is int32 [B, k]")
-    k = slots.shape[1]
-    _need_dense(slots)
-    out, lse = _attention_args(q, sink, gate, out, out_dtype, lse, want_lse)
-    if B > 0 and H > 0:
-        if workspace is None:
-            workspace = _workspace(None, _abi.ic_latent_sparse_workspace_size(B, H, k), q.device)
-        else:
-            _workspace(workspace, 0, q.device)
-        _abi.ic_latent_sparse_decode(q.data_ptr(), cache.data_ptr(), P, ps, stride, slots.data_ptr(), k, _addr(sink),
-                                     _addr(gate), _SM_SCALE if sm_scale is None else sm_scale, B, H,
-                                     _OUT_DTYPE[out.dtype], out.data_ptr(), _addr(lse), workspace.data_ptr(),
-                                     workspace.numel(), _current_stream(dev))
-    return out, lse
+            return latent_sparse_decode(q, cache, slots, sink, gate, sm_scale, out_dtype, out, lse, want_lse, workspace)
+    return _front.latent_sparse_decode(q, cache, slots, sink, gate, _SM_SCALE if sm_scale is None else sm_scale,
+                                       _code(_OUT_DTYPE, out_dtype, "out is bf16 or fp32"), out, lse, want_lse,
+                                       workspace)
 
 
 def slots_of(idx: torch.Tensor, block_table: torch.Tensor, page_size: int) -> torch.Tensor:
