@@ -421,10 +421,10 @@ bool paged_cache_ok(const void* cache, ic_dtype_t dtype, int64_t num_pages, int 
 }
 
 // Shares of the tiles: one CTA per SM for the blocks of query rows of each
-// share, but no more shares than two-tile pieces of the longest contexts.
+// share, but no more shares than tiles of the longest contexts.
 int latent_groups(int64_t max_tiles, int rblocks) {
   const int64_t g = std::max(1, num_sms() / rblocks);
-  return static_cast<int>(std::min<int64_t>(g, std::max<int64_t>(1, ceil_div<int64_t>(max_tiles, 2))));
+  return static_cast<int>(std::min<int64_t>(g, std::max<int64_t>(1, max_tiles)));
 }
 
 struct LatentLayout {

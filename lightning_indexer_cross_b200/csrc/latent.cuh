@@ -14,7 +14,6 @@ namespace {
 constexpr int kT = kLatentTile;
 constexpr int kSlab = kT * 128;       // 64 rows x 64 dims, bf16
 constexpr int kTile = 9 * kSlab;      // 64 rows of 576 dims: slabs 0-7 latent, 8 rotary
-constexpr int kMinTiles = 2;          // tiles of a group, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.f;          // log2 units by which a row's maximum may pass its reference
 
@@ -61,16 +60,15 @@ IC_DEV int64_t share_start(int g, int64_t total, int G) {
   return g * total / G;
 }
 IC_DEV int eff_groups(int groups, int64_t tiles) {
-  const int64_t g = (tiles + kMinTiles - 1) / kMinTiles;
-  return g < groups ? static_cast<int>(g) : groups;
+  return tiles < groups ? static_cast<int>(tiles) : groups;
 }
 
 // One warp finds the tiles of its group's share, publishes their descriptors and
 // asks L2 for their rows: all of them, or (half >= 0) those of one half of a
 // tile, where the other CTA of the pair asks for the rest. unit: rows of an entry
-// of TileInfo::at.
+// of TileInfo::at. len0: the length of sequence `lane`, read while the CTA set up.
 template <bool FP8, bool SPARSE, int kInfo, class Wait>
-IC_DEV void find_tiles(const LatentArgs& a, int group, int unit, int half, TileInfo* infos, int64_t* places,
+IC_DEV void find_tiles(const LatentArgs& a, int64_t len0, int group, int unit, int half, TileInfo* infos, int64_t* places,
                        uint64_t* info_full, uint64_t* info_free, Wait wait) {
   const int lane = threadIdx.x & 31;
   // lane l holds the length of sequence cb + l
@@ -82,7 +80,7 @@ IC_DEV void find_tiles(const LatentArgs& a, int group, int unit, int half, TileI
     total = static_cast<int64_t>(a.B) * tiles_of(a.k);
   } else {
     for (cb = 0; cb < a.B; cb += 32) {
-      const int64_t n = cb + lane < a.B ? a.lens[cb + lane] : 0;
+      const int64_t n = cb == 0 ? len0 : cb + lane < a.B ? a.lens[cb + lane] : 0;
       if (n != clamp_len(a, n)) record_status(a.status, IC_ERR_BAD_INDEX);
       clen = static_cast<int>(clamp_len(a, n));
       total += tiles_of(clen);

@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
     fence_mbar_init();
   }
   pdl_wait();
+  const int64_t len0 = !SPARSE && warp == 0 && lane < a.B ? a.lens[lane] : 0;
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ tiles
-    find_tiles<FP8, SPARSE, kInfo>(a, group, FP8 ? 16 : br, -1, infos, places, info_full, info_free, wait);
+    find_tiles<FP8, SPARSE, kInfo>(a, len0, group, FP8 ? 16 : br, -1, infos, places, info_full, info_free, wait);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q . K^T
     constexpr uint32_t idesc = idesc_bf16_f32(M, kT, false, false);

@@ -114,16 +114,19 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 // kRowsPerWarp consecutive rows; lane j < kRowsPerWarp finds the place of row j,
 // so that the lookups of a warp are one chain: the sequence (32 probes a step),
 // the page, the rows.
-constexpr int kRowsPerWarp = 8;
-constexpr int kBatch = 4;  // rows in flight
+constexpr int kRowsMost = 8;  // rows of a warp: 4, or 8 where that many warps fill the SMs twice
+constexpr int kBatch = 4;     // rows in flight
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadArgs a) {
+__global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadArgs a, int rpw) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsPerWarp;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * rpw;
   int64_t end = a.cu[a.B];
+  // up to 32 sequences: lane b has cu[b], and the lookups need no other read
+  const bool few = a.B <= 32;
+  const int64_t cu0 = few && lane < a.B ? a.cu[lane] : 0;
   // the last b with cu[b] <= r0 lies in [lo, lo + n)
-  int lo = 0, n = a.B;
+  int lo = 0, n = few ? 1 : a.B;
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int at = lo + lane * step;
@@ -138,12 +141,21 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadA
     end = a.R;
   }
   if (r0 >= end) return;
+  int b = lo;
+  int64_t first = 0;  // lane j: the sequence of row j, and its first row
+  if (few) {
+    for (int j = 0; j < rpw; ++j) {
+      const uint32_t m = __ballot_sync(0xffffffffu, lane < a.B && cu0 <= r0 + j) | 1u;
+      if (lane == j) b = 31 - __clz(m);
+    }
+    first = __shfl_sync(0xffffffffu, cu0, b);
+  } else if (lane < rpw) {
+    while (b + 1 < a.B && a.cu[b + 1] <= r0 + lane) ++b;
+    first = a.cu[b];
+  }
   int64_t from = -1;  // lane j: byte offset of row j
-  if (lane < kRowsPerWarp && r0 + lane < end) {
-    int b = lo;
-    const int64_t r = r0 + lane;
-    while (b + 1 < a.B && a.cu[b + 1] <= r) ++b;
-    const int64_t p = r - a.cu[b];
+  if (lane < rpw && r0 + lane < end) {
+    const int64_t p = r0 + lane - first;
     if (p >= 0 && p < static_cast<int64_t>(a.table_width) * a.page_size) {
       const int64_t pi = p / a.page_size;
       const int page = a.table[static_cast<int64_t>(b) * a.table_stride + pi];
@@ -153,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadA
     if (from < 0) record_status(a.status, IC_ERR_BAD_INDEX);
   }
 #pragma unroll 1
-  for (int j0 = 0; j0 < kRowsPerWarp; j0 += kBatch) {
+  for (int j0 = 0; j0 < rpw; j0 += kBatch) {
     const int64_t rb = r0 + j0;
     if (rb >= end) return;
     const uint8_t* src[kBatch];
@@ -227,12 +239,13 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a, bool fp8, cudaStream
 }
 
 cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t stream) {
-  constexpr int kRows = kWarps * kRowsPerWarp;
-  const unsigned grid = static_cast<unsigned>((a.R + kRows - 1) / kRows);
+  const int rpw = a.R > 148 * 2 * kWarps * kRowsMost ? kRowsMost : kBatch;
+  const int rows = kWarps * rpw;
+  const unsigned grid = static_cast<unsigned>((a.R + rows - 1) / rows);
   if (fp8)
-    latent_read_kernel<true><<<grid, kThreads, 0, stream>>>(a);
+    latent_read_kernel<true><<<grid, kThreads, 0, stream>>>(a, rpw);
   else
-    latent_read_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+    latent_read_kernel<false><<<grid, kThreads, 0, stream>>>(a, rpw);
   return cudaGetLastError();
 }
 

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
     fence_mbar_init();
   }
   pdl_wait();
+  const int64_t len0 = !SPARSE && warp == 0 && lane < a.B ? a.lens[lane] : 0;
   // the swizzled layouts need a 1024-byte-aligned base (the same in both CTAs)
   const bool aligned = (smem_u32(smem) & 1023u) == 0;
   if (!aligned && threadIdx.x == 0) record_status(a.status, IC_ERR_UNSUPPORTED);
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
   if (!aligned) {
     // (nothing runs)
   } else if (warp == 0) {
-    find_tiles<FP8, SPARSE, kInfo>(a, group, 16, rank, infos, places, info_full, info_free, wait);
+    find_tiles<FP8, SPARSE, kInfo>(a, len0, group, 16, rank, infos, places, info_full, info_free, wait);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q . K^T
     constexpr uint32_t idesc = idesc_bf16_f32(128, kT, false, false);
