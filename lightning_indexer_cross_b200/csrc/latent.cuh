@@ -307,48 +307,48 @@ IC_DEV void softmax_rows(const LatentArgs& a, uint32_t tmem, uint8_t* ps, float*
     uint32_t pk[kCols / 2];
     float sum = 0.f;
     auto weigh = [&](float base) {
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int j = 0; j < kCols; j += 2) {
-        const float p0 = ex2_approx(fmaf(__uint_as_float(rv[j]), c2, -base));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(rv[j + 1]), c2, -base));
-        part[(j >> 1) & 3] += p0 + p1;
-        pk[j >> 1] = pack_bf16x2(p0, p1);
+        const float2 z = fma2(make_float2(__uint_as_float(rv[j]), __uint_as_float(rv[j + 1])), make_float2(c2, c2),
+                              make_float2(-base, -base));
+        const float2 w = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+        part[(j >> 1) & 1] = add2(part[(j >> 1) & 1], w);
+        pk[j >> 1] = pack_bf16x2(w.x, w.y);
       }
-      sum = (part[0] + part[1]) + (part[2] + part[3]);
+      sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
     };
-    // First under the old reference, while the other parts' maxima come
-    // (most tiles leave it where it is), and again if it has moved. (A row
-    // with nothing valid so far: every weight is 0.)
-    float scale = 1.f;
-#pragma unroll 1
-    for (int pass = 0;; ++pass) {
-      weigh(ref == -INFINITY ? 0.f : ref);
-      if (pass) break;
-      float other[R::kParts];
-      ok = take(other);
-      float m = other[0];
-#pragma unroll
-      for (int i = 1; i < R::kParts; ++i) m = fmaxf(m, other[i]);
-      m *= c2;
-      // the reference moves when the row's maximum passes it by more than
-      // kMove: weights stay below 2^8, far from bf16's and fp32's limits
-      bool moved = false;
-      if (ref == -INFINITY) {
-        moved = m != -INFINITY;
-        ref = m;
-      } else if (m > ref + kMove) {
-        scale = ex2_approx(ref - m);
-        ref = m;
-        moved = true;
-      }
-      if (!__any_sync(0xffffffffu, moved)) break;
-    }
+    // Under the old reference first, which most tiles leave where it is; the
+    // other parts' maxima are looked at once everything else has been waited
+    // for. (A row with nothing valid so far: every weight is 0.)
+    weigh(ref == -INFINITY ? 0.f : ref);
+    const TileInfo y = x;
+    ok = get_info(t + 1, x);
     if (!ok) break;
-    l = fmaf(l, scale, sum);
     // the product that used this buffer has read its weights
     if (t >= R::kPBufs) ok = wait(&pv_done[(t - R::kPBufs) & 1], ((t - R::kPBufs) >> 1) & 1);
     if (!ok) break;
+    float other[R::kParts];
+    ok = take(other);
+    if (!ok) break;
+    float m = other[0];
+#pragma unroll
+    for (int i = 1; i < R::kParts; ++i) m = fmaxf(m, other[i]);
+    m *= c2;
+    // the reference moves when the row's maximum passes it by more than kMove:
+    // weights stay below 2^8, far from bf16's and fp32's limits
+    float scale = 1.f;
+    bool moved = false;
+    if (ref == -INFINITY) {
+      moved = m != -INFINITY;
+      ref = m;
+    } else if (m > ref + kMove) {
+      scale = ex2_approx(ref - m);
+      ref = m;
+      moved = true;
+    }
+    if (__any_sync(0xffffffffu, moved)) weigh(ref == -INFINITY ? 0.f : ref);
+    l = fmaf(l, scale, sum);
     if (__any_sync(0xffffffffu, scale != 1.f)) {  // (then t > 0, and the warps of a row agree)
       ok = wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);  // O stands still
       if (!ok) break;
@@ -372,9 +372,6 @@ IC_DEV void softmax_rows(const LatentArgs& a, uint32_t tmem, uint8_t* ps, float*
     fence_proxy_async_smem();
     tc_fence_before();
     p_arrive(t);
-    TileInfo y = x;
-    ok = get_info(t + 1, x);
-    if (!ok) break;
     if (!(y.flags & kLast)) continue;
     // ---- Q of the next piece, and this one's output
     if (M == 32 && !(x.flags & kEnd)) {
