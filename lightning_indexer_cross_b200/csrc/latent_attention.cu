@@ -390,23 +390,23 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
     // (64-byte pieces of eight rows cost four times the lookups in L1, which then
     // bound the kernel). Eight lanes that store together have four words of two
     // neighbouring slabs; those of the odd slab store their second half first, so
-    // the eight meet eight chunks of the swizzle. The next unit's loads are in
-    // flight while one is widened.
+    // the eight meet eight chunks of the swizzle. Both units are on their way at
+    // once: one's next loads are issued as soon as its registers are read.
     const int w = warp - 8;
     struct Unit {
       uint4 code[4], rot;  // rot: word lane & 7 of row lane >> 3
       float scale;         // lane l < 16: group l & 3 of row l >> 2
-    } cur, nxt;
+    } u0, u1;
     const int odd = (lane >> 2) & 1, wch = lane & 3;
-    TileInfo x;
-    int ring = 0;  // descriptor slot of x
+    TileInfo x;  // of the tile that is loaded
+    int ring = 0;  // its descriptor slot
     auto fetch = [&](int t) {
       ring = t % kInfo;
       if (!wait(&info_full[ring], (t / kInfo) & 1)) return false;
       x = infos[ring];
       return true;
     };
-    auto load = [&](int h) {  // rows 8 w + 4 h + [0, 4) of x's tile
+    auto load = [&](Unit& v, int h) {  // rows 8 w + 4 h + [0, 4) of x's tile
       const int r0 = 8 * w + 4 * h;
       const uint32_t m = (w & 4 ? x.mask[1] : x.mask[0]) >> (r0 & 31);
       const uint8_t* base = a.cache;  // dense: the first of the four rows
@@ -416,75 +416,38 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
         if constexpr (SPARSE) return a.cache + places[ring * kT + r0 + j];
         else return base + j * kLatentRowFp8;
       };
-      nxt.scale = 1.f;
-      nxt.rot = make_uint4(0, 0, 0, 0);
-      if (lane < 16 && ((m >> (lane >> 2)) & 1u)) nxt.scale = ld_nc_f(row_of(lane >> 2) + 512 + (lane & 3) * 4);
+      v.scale = 1.f;
+      v.rot = make_uint4(0, 0, 0, 0);
+      if (lane < 16 && ((m >> (lane >> 2)) & 1u)) v.scale = ld_nc_f(row_of(lane >> 2) + 512 + (lane & 3) * 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        nxt.code[j] = make_uint4(0, 0, 0, 0);
-        if ((m >> j) & 1u) nxt.code[j] = ld_nc_v4(row_of(j) + lane * 16);
+        v.code[j] = make_uint4(0, 0, 0, 0);
+        if ((m >> j) & 1u) v.code[j] = ld_nc_v4(row_of(j) + lane * 16);
       }
-      if ((m >> (lane >> 3)) & 1u) nxt.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
+      if ((m >> (lane >> 3)) & 1u) v.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
     };
-    bool ok = fetch(0);
-    bool more = ok && !(x.flags & kEnd);
-    if (more) load(0);
-    int n = 0, b = x.b, qn = -1;  // qn: stage of the last Q that this warp has copied
-    bool first = true;
     uint32_t tile = 0;
-#pragma unroll 1
-    for (int u = 0; more; ++u) {
-      const int t = u >> 1, h = u & 1;
-      if (h == 0) {
-        // Every warp waits for every stage, Q's too, which the first of them
-        // copies: a warp that skipped one could be two phases ahead at its next
-        // wait, and take an older phase of the same parity for its own.
-        if (kQStage && first) {
-          const int qs = n % kStages;
-          ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
-          if (!ok) break;
-          if (w == 0) {
-            if (lane == 0) {
-              mbar_arrive_n(&full[qs], 7);
-              mbar_arrive_expect_tx(&full[qs], 9 * R::kQSlab);
-            }
-            __syncwarp();
-            copy_q(b, smem + qs * kTile, &full[qs]);
-            qn = n;
-          }
-          ++n;
-        }
-        tile = smem_u32(smem) + (n % kStages) * kTile;
-      }
+    int n = 0, b = 0, qn = -1;  // qn: stage of the last Q that this warp has copied
+    bool more = false, first = true;
+    // widens one unit into the tile in stage n; once its registers are read,
+    // `then` asks for what they hold next
+    auto widen = [&](Unit& v, int h, auto&& then) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) use_now(nxt.code[j]);  // the unit has arrived
-      use_now(nxt.rot);
-      cur = nxt;
-      if (h == 0) {
-        load(1);
-        warp_arrive(&info_free[ring]);
-      } else {
-        ok = fetch(t + 1);
-        if (!ok) break;
-        more = !(x.flags & kEnd);
-        first = (x.flags & kFirst) != 0;
-        b = x.b;
-        if (more) load(0);
-      }
+      for (int j = 0; j < 4; ++j) use_now(v.code[j]);  // the unit has arrived
+      use_now(v.rot);
       // all four rows at once, with nothing ordered in between: two warps a
       // scheduler leave it to one warp's independent instructions to fill it
       uint32_t o[4][8];
       float f[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = __shfl_sync(0xffffffffu, cur.scale, 4 * j + (lane >> 3));
+      for (int j = 0; j < 4; ++j) f[j] = __shfl_sync(0xffffffffu, v.scale, 4 * j + (lane >> 3));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e4m3x16_to_bf16x16(cur.code[j], f[j], o[j]);
-      if (h == 0) {
-        ok = wait(&freed[n % kStages], ((n / kStages) & 1) ^ 1);
-        if (!ok) break;
-      }
+      for (int j = 0; j < 4; ++j) e4m3x16_to_bf16x16(v.code[j], f[j], o[j]);
+      const uint4 rot = v.rot;
+      if (!then()) return false;
+      if (h == 0 && !wait(&freed[n % kStages], ((n / kStages) & 1) ^ 1)) return false;
       const int r0 = 8 * w + 4 * h;
-      st_shared_v4(tile + 8 * kSlab + sw128_offset(r0 + (lane >> 3), lane & 7), cur.rot);
+      st_shared_v4(tile + 8 * kSlab + sw128_offset(r0 + (lane >> 3), lane & 7), rot);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint4 lo = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]), hi = make_uint4(o[j][4], o[j][5], o[j][6], o[j][7]);
@@ -492,11 +455,59 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
         st_shared_v4(dst + sw128_offset(r0 + j, 2 * wch + odd), odd ? hi : lo);
         st_shared_v4(dst + sw128_offset(r0 + j, 2 * wch + 1 - odd), odd ? lo : hi);
       }
-      if (h == 1) {
-        fence_proxy_async_smem();
-        warp_arrive(&full[n % kStages]);
+      return true;
+    };
+    bool ok = fetch(0);
+    if (ok) {
+      more = !(x.flags & kEnd);
+      b = x.b;
+      if (more) {
+        load(u0, 0);
+        load(u1, 1);
+        warp_arrive(&info_free[ring]);
+      }
+    }
+#pragma unroll 1
+    for (int t = 0; more; ++t) {
+      // Every warp waits for every stage, Q's too, which the first of them
+      // copies: a warp that skipped one could be two phases ahead at its next
+      // wait, and take an older phase of the same parity for its own.
+      if (kQStage && first) {
+        const int qs = n % kStages;
+        ok = wait(&freed[qs], ((n / kStages) & 1) ^ 1);
+        if (!ok) break;
+        if (w == 0) {
+          if (lane == 0) {
+            mbar_arrive_n(&full[qs], 7);
+            mbar_arrive_expect_tx(&full[qs], 9 * R::kQSlab);
+          }
+          __syncwarp();
+          copy_q(b, smem + qs * kTile, &full[qs]);
+          qn = n;
+        }
         ++n;
       }
+      tile = smem_u32(smem) + (n % kStages) * kTile;
+      ok = widen(u0, 0, [&] {
+        if (!fetch(t + 1)) return false;
+        more = !(x.flags & kEnd);
+        first = (x.flags & kFirst) != 0;
+        b = x.b;
+        if (more) load(u0, 0);
+        return true;
+      });
+      if (!ok) break;
+      ok = widen(u1, 1, [&] {
+        if (more) {
+          load(u1, 1);
+          warp_arrive(&info_free[ring]);
+        }
+        return true;
+      });
+      if (!ok) break;
+      fence_proxy_async_smem();
+      warp_arrive(&full[n % kStages]);
+      ++n;
     }
     // given up: the copy lands before the CTA exits (else the piece's products have waited for it)
     if (!ok && qn >= 0 && lane == 0) mbar_drain(&full[qn % kStages], (qn / kStages) & 1);
