@@ -310,7 +310,7 @@ IC_DEV void softmax_rows(const LatentArgs& a, uint32_t tmem, uint8_t* ps, float*
       float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int j = 0; j < kCols; j += 2) {
-        const float2 z = fma2(make_float2(__uint_as_float(rv[j]), __uint_as_float(rv[j + 1])), make_float2(c2, c2),
+        const float2 z = ffma2(make_float2(__uint_as_float(rv[j]), __uint_as_float(rv[j + 1])), make_float2(c2, c2),
                               make_float2(-base, -base));
         const float2 w = make_float2(ex2_approx(z.x), ex2_approx(z.y));
         part[(j >> 1) & 1] = add2(part[(j >> 1) & 1], w);

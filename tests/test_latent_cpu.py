@@ -241,3 +241,12 @@ def test_slots_of_maps_positions_through_the_table(ops):
     got = ops.slots_of(idx, table, 16)
     assert got.dtype == torch.int32
     assert got.tolist() == [[112, 127, 48, 88, -1], [33, -1, -1, 2, 31]]
+
+
+def test_slots_of_gives_no_cached_slot_past_the_table_or_for_pages_below_zero(ops):
+    table = torch.tensor([[7, -1]], dtype=torch.int32)
+    none = 2 ** 31 - 1
+    idx = torch.tensor([[15, 16, 31, 32, 2 ** 31 - 1, -1]], dtype=torch.int32)
+    assert ops.slots_of(idx, table, 16).tolist() == [[127, none, none, none, none, -1]]
+    with pytest.raises(ValueError):
+        ops.slots_of(idx, table[:, :0], 16)
