@@ -13,27 +13,35 @@
 // out evenly: group g takes tiles [g T / G, (g + 1) T / G), so ragged lengths
 // load every SM alike and a single long sequence uses all of them. The lengths
 // are read on the device; nothing waits for the host. A group has one CTA for
-// each block of 32 query rows; the CTAs of a group read the same tiles at the
-// same time, so the second read of a tile hits L2. A piece is what one group
-// has of one sequence: whole sequences are finished by their CTA, the others
-// leave (reference, sum, unnormalised output) in fp32 and a second kernel
-// joins them.
+// each block of query rows (32 rows, or 64 of 33 to 64; above that pairs of CTAs
+// take 128, latent_pair.cu). A piece is what one group has of one sequence:
+// whole sequences are finished by their CTA, the others leave (reference, sum,
+// unnormalised output) in fp32 and a second kernel joins them.
 //
-// CTA. M = 32 query rows in the weight-stationary MMA form: lane quadrant q of
-// TMEM holds the 32 rows' columns [q N / 4, (q + 1) N / 4), and Q, an operand
-// in TMEM, is there once in each quadrant. Per tile
-//   S[32 x 64]   = Q . K^T         (36 MMAs, N = 64)
-//   P            = 2^(S sm_scale log2e - ref), bf16 into shared memory
-//   O[32 x 512] += P . V           (8 MMAs, N = 256; V is the same tile read
-//                                   as an MN-major operand)
+// CTA. M query rows in the weight-stationary MMA form. M = 32: lane quadrant q
+// of TMEM holds the 32 rows' columns [q N / 4, (q + 1) N / 4), and Q, an operand
+// in TMEM, is there once in each quadrant; it enters through a tile's stage, so
+// that three tiles fit. M = 64: lanes 0-63 hold the first half of the columns,
+// 64-127 the second; Q stays in shared memory (72 KB) beside two tiles. Per tile
+//   S[M x 64]   = Q . K^T         (36 MMAs, N = 64)
+//   P           = 2^(S sm_scale log2e - ref), bf16 into shared memory
+//   O[M x 512] += P . V           (8 MMAs, N = 256; V is the same tile read
+//                                  as an MN-major operand)
 // with the running reference of an online softmax, moved (and O rescaled) only
 // when a row's maximum passes it by more than 2^8.
 //
-// What bounds it. A tile is written to shared memory (72 KB) and read twice by
-// the MMAs (144 KB): 1720 cycles at 128 bytes a cycle. With Q in shared memory
-// too the S products would read as much again and saturate it, and every
-// mbarrier and softmax access would queue behind them; without it there is room
-// for a third tile.
+// What bounds it. The MMAs of a tile take 1600 cycles at M = 32 (28 and 76 a
+// product, measured) and 1800 at M = 64 (32 and 80); the bytes of an e4m3 tile,
+// 42 KB, are 1800 cycles of an SM's share of HBM. Measured, a tile takes 3000
+// cycles of e4m3 (4 sequences of 54K rows on average, 32 query rows: 65 us with
+// 8 us of joining; 2.5 TB/s before it): the widening warps need 1200 of issue alone, and the
+// rest is the latency of their chain (descriptor, loads, conversion, stores, fence)
+// with two warps a scheduler. Converting with a quarter fewer instructions, and
+// counting the rings' places along instead of dividing, gave 3 % together; a second
+// set of widening warps has no registers left. A bf16 tile takes as long as its
+// chain QK -> softmax -> PV, of which two tiles are under way. Small calls (one
+// sequence of a few hundred rows, 12 us) are two launches, the setup of a CTA
+// (barriers, TMEM, lengths: 5000 cycles to the first product), one tile and the join.
 //
 // Roles. Warp 0 finds the tiles, up to kInfo ahead, and asks L2 for them;
 // warps 1 and 2 issue the two products, each as soon as its own inputs are
@@ -41,8 +49,8 @@
 // 3 issues TMA boxes that land in the operand layout, warp 8 clears the rows
 // behind a sequence's end (a zero weight times a NaN left there would be NaN).
 // e4m3 pages: warps 8-15 take a tile's codes to registers, straight from L2, and
-// widen them into the operand layout (staging them in shared memory would add
-// 84 KB to its traffic).
+// widen them into the operand layout (there is no room to stage them in shared
+// memory).
 #include "latent.cuh"
 
 namespace ic {
@@ -697,7 +705,9 @@ cudaError_t launch_one(const CUtensorMap& qmap, const CUtensorMap& kvmap, const 
 
 template <bool SPARSE, int M>
 cudaError_t launch_join(const LatentArgs& a, cudaStream_t stream) {
-  // pieces of a sequence: about groups / B + 1
+  // Pieces of a sequence: about groups / B + 1. More than four are shared by eight
+  // warps: 38 pieces of 4 sequences x 32 rows take 8 us so, 45 by one warp each; with
+  // three or four pieces both are within 0.5 us, and one warp needs no shared memory.
   const bool many = a.groups / a.B + 1 > 4;
   const unsigned ctas = static_cast<unsigned>(a.B) * ((a.rows + 31) / 32) * (many ? 32 : 4);
   auto join = many ? latent_join_kernel<SPARSE, M, 8> : latent_join_kernel<SPARSE, M, 1>;

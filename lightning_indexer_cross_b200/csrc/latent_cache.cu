@@ -12,8 +12,11 @@
 // to e4m3 (nearest even, at most half a step, 2^-4 of the value), and a reader
 // may form the products of a row in bf16 without a second one.
 //
-// Both kernels move each byte once, one warp a token with 16-byte words, and
-// are bound by HBM for long runs and by launch latency at decode sizes.
+// Both kernels move each byte once with whole-line accesses, one warp a token,
+// and are bound by HBM for long runs (read-back of 82K e4m3 rows: 27 us, 5.4 TB/s
+// of 656 bytes read and 1152 written a row; 16384 rows appended: 8.3 us, 3.6 TB/s,
+// launch and the angles' latency among it) and by launch latency at decode sizes
+// (32 rows: 4 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -111,16 +114,16 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 }
 
 // Output row r belongs to sequence b with cu[b] <= r < cu[b + 1]. A warp takes
-// kRowsPerWarp consecutive rows; lane j < kRowsPerWarp finds the place of row j,
-// so that the lookups of a warp are one chain: the sequence (32 probes a step),
-// the page, the rows.
-constexpr int kRowsMost = 8;  // rows of a warp: 4, or 8 where that many warps fill the SMs twice
-constexpr int kBatch = 4;     // rows in flight
+// kRows consecutive rows; lane j < kRows finds the place of row j, so that the
+// lookups of a warp are one chain: the sequence (32 probes a step, or none up to
+// 32 sequences), the page, the rows. 82K e4m3 rows: 27.4 us, 29.0 with 8 rows a
+// warp in two batches; 3 sequences of up to 1021 bf16 rows: 4.3 and 6.3 us.
+constexpr int kRows = 4;
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadArgs a, int rpw) {
+__global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * rpw;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows;
   int64_t end = a.cu[a.B];
   // up to 32 sequences: lane b has cu[b], and the lookups need no other read
   const bool few = a.B <= 32;
@@ -144,17 +147,18 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadA
   int b = lo;
   int64_t first = 0;  // lane j: the sequence of row j, and its first row
   if (few) {
-    for (int j = 0; j < rpw; ++j) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
       const uint32_t m = __ballot_sync(0xffffffffu, lane < a.B && cu0 <= r0 + j) | 1u;
       if (lane == j) b = 31 - __clz(m);
     }
     first = __shfl_sync(0xffffffffu, cu0, b);
-  } else if (lane < rpw) {
+  } else if (lane < kRows) {
     while (b + 1 < a.B && a.cu[b + 1] <= r0 + lane) ++b;
     first = a.cu[b];
   }
   int64_t from = -1;  // lane j: byte offset of row j
-  if (lane < rpw && r0 + lane < end) {
+  if (lane < kRows && r0 + lane < end) {
     const int64_t p = r0 + lane - first;
     if (p >= 0 && p < static_cast<int64_t>(a.table_width) * a.page_size) {
       const int64_t pi = p / a.page_size;
@@ -164,66 +168,61 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadA
     }
     if (from < 0) record_status(a.status, IC_ERR_BAD_INDEX);
   }
-#pragma unroll 1
-  for (int j0 = 0; j0 < rpw; j0 += kBatch) {
-    const int64_t rb = r0 + j0;
-    if (rb >= end) return;
-    const uint8_t* src[kBatch];
+  const uint8_t* src[kRows];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int64_t o = __shfl_sync(0xffffffffu, from, j0 + j);
-      src[j] = o < 0 ? nullptr : static_cast<const uint8_t*>(a.cache) + o;
-    }
-    if constexpr (!FP8) {
-      // 72 words of 16 bytes a row
-      uint4 w[kBatch][3];
+  for (int j = 0; j < kRows; ++j) {
+    const int64_t o = __shfl_sync(0xffffffffu, from, j);
+    src[j] = o < 0 ? nullptr : static_cast<const uint8_t*>(a.cache) + o;
+  }
+  if constexpr (!FP8) {
+    // 72 words of 16 bytes a row
+    uint4 w[kRows][3];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
+    for (int j = 0; j < kRows; ++j)
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          w[j][k] = make_uint4(0, 0, 0, 0);
-          if (src[j] && lane + 32 * k < 72) w[j][k] = *reinterpret_cast<const uint4*>(src[j] + (lane + 32 * k) * 16);
-        }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (rb + j < end) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (rb + j) * 576);
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            if (lane + 32 * k < 72) dst[lane + 32 * k] = w[j][k];
-        }
-    } else {
-      // lane l has dims 8 l and 256 + 8 l, so that each store fills whole lines
-      uint2 c[kBatch][2];
-      uint32_t rot[kBatch];
-      float s[kBatch][2];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        rot[j] = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          c[j][k] = make_uint2(0, 0);
-          s[j][k] = 0.f;
-          if (src[j]) {
-            c[j][k] = *reinterpret_cast<const uint2*>(src[j] + k * 256 + lane * 8);
-            s[j][k] = *reinterpret_cast<const float*>(src[j] + 512 + (2 * k + (lane >> 4)) * 4);
-          }
-        }
-        if (src[j]) rot[j] = *reinterpret_cast<const uint32_t*>(src[j] + 528 + lane * 4);
+      for (int k = 0; k < 3; ++k) {
+        w[j][k] = make_uint4(0, 0, 0, 0);
+        if (src[j] && lane + 32 * k < 72) w[j][k] = *reinterpret_cast<const uint4*>(src[j] + (lane + 32 * k) * 16);
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (rb + j < end) {
-          uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + (rb + j) * 576);
+    for (int j = 0; j < kRows; ++j)
+      if (r0 + j < end) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (r0 + j) * 576);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t o[4];
-            e4m3x8_to_bf16x8(c[j][k], s[j][k], o);
-            *reinterpret_cast<uint4*>(dst + k * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          *reinterpret_cast<uint32_t*>(dst + 1024 + lane * 4) = rot[j];
+        for (int k = 0; k < 3; ++k)
+          if (lane + 32 * k < 72) dst[lane + 32 * k] = w[j][k];
+      }
+  } else {
+    // lane l has dims 8 l and 256 + 8 l, so that each store fills whole lines
+    uint2 c[kRows][2];
+    uint32_t rot[kRows];
+    float s[kRows][2];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      rot[j] = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        c[j][k] = make_uint2(0, 0);
+        s[j][k] = 0.f;
+        if (src[j]) {
+          c[j][k] = *reinterpret_cast<const uint2*>(src[j] + k * 256 + lane * 8);
+          s[j][k] = *reinterpret_cast<const float*>(src[j] + 512 + (2 * k + (lane >> 4)) * 4);
         }
+      }
+      if (src[j]) rot[j] = *reinterpret_cast<const uint32_t*>(src[j] + 528 + lane * 4);
     }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      if (r0 + j < end) {
+        uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + (r0 + j) * 576);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t o[4];
+          e4m3x8_to_bf16x8(c[j][k], s[j][k], o);
+          *reinterpret_cast<uint4*>(dst + k * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        *reinterpret_cast<uint32_t*>(dst + 1024 + lane * 4) = rot[j];
+      }
   }
 }
 
@@ -239,13 +238,12 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a, bool fp8, cudaStream
 }
 
 cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t stream) {
-  const int rpw = a.R > 148 * 2 * kWarps * kRowsMost ? kRowsMost : kBatch;
-  const int rows = kWarps * rpw;
+  const int rows = kWarps * kRows;
   const unsigned grid = static_cast<unsigned>((a.R + rows - 1) / rows);
   if (fp8)
-    latent_read_kernel<true><<<grid, kThreads, 0, stream>>>(a, rpw);
+    latent_read_kernel<true><<<grid, kThreads, 0, stream>>>(a);
   else
-    latent_read_kernel<false><<<grid, kThreads, 0, stream>>>(a, rpw);
+    latent_read_kernel<false><<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
