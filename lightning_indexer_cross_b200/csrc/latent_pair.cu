@@ -193,81 +193,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
   };
   const int br = a.page_size % 32 == 0 ? 32 : 16;  // rows of a TMA box
 
-  if (!aligned) {
-    // (nothing runs)
-  } else if (warp == 0) {
-    find_tiles<FP8, SPARSE, kInfo>(a, len0, group, 16, rank, infos, places, info_full, info_free, wait);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S = Q . K^T
-    constexpr uint32_t idesc = idesc_bf16_f32(128, kT, false, false);
-    int pieces = 0;
-#pragma unroll 1
-    for (int t = 0;; ++t) {
-      TileInfo x;
-      if (!get_info(t, x) || (x.flags & kEnd)) break;
-      if (rank != 0) continue;
-      if (x.flags & kFirst) {
-        if (!wait(q_full, pieces & 1)) break;
-        ++pieces;
-      }
-      // the logits of tile t - 2 have been read
-      if (t >= 2 && !wait(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
-      if (!wait(&k_full[t & 1], (t >> 1) & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tmem + R64::kSCol + (t & 1) * R64::kCols;
-        const uint64_t ad = sw128_desc(smem_u32(qs), 16, 1024), bd = sw128_desc(smem_u32(ks) + (t & 1) * kKBytes, 16, 1024);
-#pragma unroll 1
-        for (int c = 0; c < 9; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_pair_bf16_ss(d, ad + c * (R64::kQSlab >> 4) + kk * 2, bd + c * (4096 >> 4) + kk * 2, idesc, c + kk > 0);
-        commit_both(&s_full[t & 1]);
-        if (x.flags & kLast) commit_both(q_free);
-      }
-      __syncwarp();
-    }
-    // every MMA issued has retired before TMEM is released
-    if (rank == 0) {
-      if (elect_one()) commit_pair(retire);
-      __syncwarp();
-      mbar_drain(retire, 0);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P . V
-    constexpr uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
-    int pieces = 0;
-#pragma unroll 1
-    for (int t = 0;; ++t) {
-      TileInfo x;
-      if (!get_info(t, x) || (x.flags & kEnd)) break;
-      if (rank != 0) continue;
-      const bool first = (x.flags & kFirst) != 0;
-      if (first) {
-        if (pieces > 0 && !wait(o_free, (pieces - 1) & 1)) break;
-        ++pieces;
-      }
-      if (!wait(&v_full[t & 1], (t >> 1) & 1)) break;
-      if (!wait(&p_ready[t & 1], (t >> 1) & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t vd = sw128_desc(smem_u32(vs) + (t & 1) * kVBytes, kSlab, 1024), pd = sw128_desc(smem_u32(ps), 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_pair_bf16_ss(tmem + R64::kOutCol + h * 128, pd + kk * 2, vd + h * (2 * kSlab >> 4) + kk * 128, idesc,
-                             !first || kk > 0);
-        commit_both(&pv_done[t & 1]);
-      }
-      __syncwarp();
-    }
-    if (rank == 0) {
-      if (elect_one()) commit_pair(retire);
-      __syncwarp();
-      mbar_drain(retire, 0);
-    }
-  } else if (warp == (FP8 ? 3 : 9)) {
+  auto load_q = [&] {
     // ------------------------------------------------------------ Q of each piece
     int pieces = 0;
     for (int t = 0;; ++t) {
@@ -288,52 +214,134 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
       tell_first(q_full);
     }
     if (pieces > 0) mbar_drain(q_landed, (pieces - 1) & 1);
-  } else if (warp >= 4 && warp < 8) {
+  };
+
+  if (!aligned) {
+    // (nothing runs)
+  } else if (warp < 4) {
+    if (warp == 0) {
+      find_tiles<FP8, SPARSE, kInfo>(a, len0, group, 16, rank, infos, places, info_full, info_free, wait);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ S = Q . K^T
+      constexpr uint32_t idesc = idesc_bf16_f32(128, kT, false, false);
+      int pieces = 0;
+#pragma unroll 1
+      for (int t = 0;; ++t) {
+        TileInfo x;
+        if (!get_info(t, x) || (x.flags & kEnd)) break;
+        if (rank != 0) continue;
+        if (x.flags & kFirst) {
+          if (!wait(q_full, pieces & 1)) break;
+          ++pieces;
+        }
+        // the logits of tile t - 2 have been read
+        if (t >= 2 && !wait(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
+        if (!wait(&k_full[t & 1], (t >> 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + R64::kSCol + (t & 1) * R64::kCols;
+          const uint64_t ad = sw128_desc(smem_u32(qs), 16, 1024), bd = sw128_desc(smem_u32(ks) + (t & 1) * kKBytes, 16, 1024);
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_pair_bf16_ss(d, ad + c * (R64::kQSlab >> 4) + kk * 2, bd + c * (4096 >> 4) + kk * 2, idesc, c + kk > 0);
+          commit_both(&s_full[t & 1]);
+          if (x.flags & kLast) commit_both(q_free);
+        }
+        __syncwarp();
+      }
+      // every MMA issued has retired before TMEM is released
+      if (rank == 0) {
+        if (elect_one()) commit_pair(retire);
+        __syncwarp();
+        mbar_drain(retire, 0);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ O += P . V
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
+      int pieces = 0;
+#pragma unroll 1
+      for (int t = 0;; ++t) {
+        TileInfo x;
+        if (!get_info(t, x) || (x.flags & kEnd)) break;
+        if (rank != 0) continue;
+        const bool first = (x.flags & kFirst) != 0;
+        if (first) {
+          if (pieces > 0 && !wait(o_free, (pieces - 1) & 1)) break;
+          ++pieces;
+        }
+        if (!wait(&v_full[t & 1], (t >> 1) & 1)) break;
+        if (!wait(&p_ready[t & 1], (t >> 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = sw128_desc(smem_u32(vs) + (t & 1) * kVBytes, kSlab, 1024), pd = sw128_desc(smem_u32(ps), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_pair_bf16_ss(tmem + R64::kOutCol + h * 128, pd + kk * 2, vd + h * (2 * kSlab >> 4) + kk * 128, idesc,
+                               !first || kk > 0);
+          commit_both(&pv_done[t & 1]);
+        }
+        __syncwarp();
+      }
+      if (rank == 0) {
+        if (elect_one()) commit_pair(retire);
+        __syncwarp();
+        mbar_drain(retire, 0);
+      }
+    } else if (!FP8 && warp == 3) {
+      // ------------------------------------------------------------ copies (bf16)
+      int nk = 0, nv = 0;
+      for (int t = 0;; ++t) {
+        TileInfo x;
+        if (!get_info(t, x) || (x.flags & kEnd)) break;
+        // boxes without a valid row read the page behind the last, which fills zeros
+        auto copy = [&](uint8_t* dst, uint64_t* bar, int i, int col) {  // 16 rows (or 32) from unit i on
+          const int pz = x.at[i] < 0 ? a.num_pages : static_cast<int>(x.at[i]);
+          tma_load_3d(dst, &kvmap, bar, col, (x.row0 + 16 * i) % a.page_size, pz);
+        };
+        const int ring = t & 1;
+        if (t >= 2 && !wait(&s_full[ring], ((t >> 1) - 1) & 1)) break;
+        if (elect_one()) {
+          uint8_t* dst = ks + ring * kKBytes;
+          mbar_arrive_expect_tx(&k_landed[ring], kKBytes);
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c) {
+            copy(dst + c * 4096, &k_landed[ring], 2 * rank, c * 64);
+            if (br == 16) copy(dst + c * 4096 + 2048, &k_landed[ring], 2 * rank + 1, c * 64);
+          }
+        }
+        __syncwarp();
+        ++nk;
+        if (t >= 2 && !wait(&pv_done[ring], ((t >> 1) - 1) & 1)) break;
+        if (elect_one()) {
+          uint8_t* dst = vs + ring * kVBytes;
+          mbar_arrive_expect_tx(&v_landed[ring], kVBytes);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (br == 16 || (i & 1) == 0) copy(dst + c * kSlab + i * 2048, &v_landed[ring], i, rank * 256 + c * 64);
+        }
+        __syncwarp();
+        ++nv;
+      }
+      // the last copies land before the CTA exits, whatever their readers do
+      for (int u = nk > 2 ? nk - 2 : 0; u < nk; ++u) mbar_drain(&k_landed[u & 1], (u >> 1) & 1);
+      for (int u = nv > 2 ? nv - 2 : 0; u < nv; ++u) mbar_drain(&v_landed[u & 1], (u >> 1) & 1);
+    } else {
+      load_q();
+    }
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax and output
     softmax_rows<64, true>(a, tmem, ps, xm, s_full, pv_done, q_free, xch, rb * kRows, rb, wait, warp_arrive, get_info,
                            [](uint32_t) { return true; }, [&](int t) { tell_first(&p_ready[t & 1]); },
                            [&]() { tell_first(o_free); });
-  } else if (!FP8 && warp == 3) {
-    // ------------------------------------------------------------ copies (bf16)
-    int nk = 0, nv = 0;
-    for (int t = 0;; ++t) {
-      TileInfo x;
-      if (!get_info(t, x) || (x.flags & kEnd)) break;
-      // boxes without a valid row read the page behind the last, which fills zeros
-      auto copy = [&](uint8_t* dst, uint64_t* bar, int i, int col) {  // 16 rows (or 32) from unit i on
-        const int pz = x.at[i] < 0 ? a.num_pages : static_cast<int>(x.at[i]);
-        tma_load_3d(dst, &kvmap, bar, col, (x.row0 + 16 * i) % a.page_size, pz);
-      };
-      const int ring = t & 1;
-      if (t >= 2 && !wait(&s_full[ring], ((t >> 1) - 1) & 1)) break;
-      if (elect_one()) {
-        uint8_t* dst = ks + ring * kKBytes;
-        mbar_arrive_expect_tx(&k_landed[ring], kKBytes);
-#pragma unroll 1
-        for (int c = 0; c < 9; ++c) {
-          copy(dst + c * 4096, &k_landed[ring], 2 * rank, c * 64);
-          if (br == 16) copy(dst + c * 4096 + 2048, &k_landed[ring], 2 * rank + 1, c * 64);
-        }
-      }
-      __syncwarp();
-      ++nk;
-      if (t >= 2 && !wait(&pv_done[ring], ((t >> 1) - 1) & 1)) break;
-      if (elect_one()) {
-        uint8_t* dst = vs + ring * kVBytes;
-        mbar_arrive_expect_tx(&v_landed[ring], kVBytes);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (br == 16 || (i & 1) == 0) copy(dst + c * kSlab + i * 2048, &v_landed[ring], i, rank * 256 + c * 64);
-      }
-      __syncwarp();
-      ++nv;
-    }
-    // the last copies land before the CTA exits, whatever their readers do
-    for (int u = nk > 2 ? nk - 2 : 0; u < nk; ++u) mbar_drain(&k_landed[u & 1], (u >> 1) & 1);
-    for (int u = nv > 2 ? nv - 2 : 0; u < nv; ++u) mbar_drain(&v_landed[u & 1], (u >> 1) & 1);
-  } else if (!FP8 && warp == 8) {
+  } else if (!FP8 && warp == 9) {
+    load_q();
+  } else if (!FP8) {
     // ------------------------------------------------------------ tiles passed on (bf16)
     for (int t = 0;; ++t) {
       TileInfo x;
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
       }
       tell_first(&v_full[ring]);
     }
-  } else if (FP8 && warp >= 8) {
+  } else {
     // ------------------------------------------------------------ widening (e4m3)
     // Warp w has four of this CTA's 32 keys of the tile: a load takes a whole
     // row's codes, lane l the 16 of word l, and they are stored as keys, and those
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
       uint4 far[2];         // word lane & 15 of this CTA's dims of the other CTA's row 2 i + (lane >> 4)
       float scale;          // lane l < 16: group l & 3 of row l >> 2
       float far_scale;      // lane l < 8: group 2 rank + (l & 1) of the other CTA's row l >> 1
-    } cur, nxt;
+    } u;
     const int odd = (lane >> 2) & 1, wch = lane & 3;
     const int r0 = 4 * w;  // first of the warp's rows among the 32
     const uint32_t vto = smem_u32(vs) + ((lane >> 2) & 3) * kSlab;
@@ -395,23 +403,23 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
           if constexpr (SPARSE) return a.cache + places[ring * kT + 32 - 32 * rank + r0 + j];
           else return fbase + j * kLatentRowFp8;
         };
-        nxt.scale = nxt.far_scale = 1.f;
-        nxt.rot = make_uint4(0, 0, 0, 0);
-        if (lane < 16 && ((m >> (lane >> 2)) & 1u)) nxt.scale = ld_nc_f(row_of(lane >> 2) + 512 + (lane & 3) * 4);
+        u.scale = u.far_scale = 1.f;
+        u.rot = make_uint4(0, 0, 0, 0);
+        if (lane < 16 && ((m >> (lane >> 2)) & 1u)) u.scale = ld_nc_f(row_of(lane >> 2) + 512 + (lane & 3) * 4);
         if (lane < 8 && ((mf >> (lane >> 1)) & 1u))
-          nxt.far_scale = ld_nc_f(far_of(lane >> 1) + 512 + (2 * rank + (lane & 1)) * 4);
+          u.far_scale = ld_nc_f(far_of(lane >> 1) + 512 + (2 * rank + (lane & 1)) * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          nxt.code[j] = make_uint4(0, 0, 0, 0);
-          if ((m >> j) & 1u) nxt.code[j] = ld_nc_v4(row_of(j) + lane * 16);
+          u.code[j] = make_uint4(0, 0, 0, 0);
+          if ((m >> j) & 1u) u.code[j] = ld_nc_v4(row_of(j) + lane * 16);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int j = 2 * i + (lane >> 4);
-          nxt.far[i] = make_uint4(0, 0, 0, 0);
-          if ((mf >> j) & 1u) nxt.far[i] = ld_nc_v4(far_of(j) + rank * 256 + (lane & 15) * 16);
+          u.far[i] = make_uint4(0, 0, 0, 0);
+          if ((mf >> j) & 1u) u.far[i] = ld_nc_v4(far_of(j) + rank * 256 + (lane & 15) * 16);
         }
-        if ((m >> (lane >> 3)) & 1u) nxt.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
+        if ((m >> (lane >> 3)) & 1u) u.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
       }
       warp_arrive(&info_free[ring]);
       return true;
@@ -421,24 +429,28 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
     for (int t = 0; ok && more; ++t) {
       const int ring = t & 1;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) use_now(nxt.code[j]);  // the tile's words have arrived
-      use_now(nxt.far[0]);
-      use_now(nxt.far[1]);
-      use_now(nxt.rot);
-      cur = nxt;
-      ok = fetch(t + 1);
-      if (!ok) break;
-      uint32_t o[4][8];
+      for (int j = 0; j < 4; ++j) use_now(u.code[j]);  // the tile's words have arrived
+      use_now(u.far[0]);
+      use_now(u.far[1]);
+      use_now(u.rot);
+      uint32_t o[4][8], of[2][8];
       float f[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = __shfl_sync(0xffffffffu, cur.scale, 4 * j + (lane >> 3));
+      for (int j = 0; j < 4; ++j) f[j] = __shfl_sync(0xffffffffu, u.scale, 4 * j + (lane >> 3));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e4m3x16_to_bf16x16(cur.code[j], f[j], o[j]);
+      for (int j = 0; j < 4; ++j) e4m3x16_to_bf16x16(u.code[j], f[j], o[j]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        e4m3x16_to_bf16x16(u.far[i], __shfl_sync(0xffffffffu, u.far_scale, 2 * (2 * i + (lane >> 4)) + ((lane >> 3) & 1)),
+                           of[i]);
+      const uint4 rot = u.rot;
+      ok = fetch(t + 1);
+      if (!ok) break;
       if (t >= 2) {
         ok = wait(&s_full[ring], ((t >> 1) - 1) & 1);  // the keys of tile t - 2 have been read
         if (!ok) break;
       }
-      st_shared_v4(smem_u32(ks) + ring * kKBytes + 8 * 4096 + sw128_offset(r0 + (lane >> 3), lane & 7), cur.rot);
+      st_shared_v4(smem_u32(ks) + ring * kKBytes + 8 * 4096 + sw128_offset(r0 + (lane >> 3), lane & 7), rot);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint4 lo = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]), hi = make_uint4(o[j][4], o[j][5], o[j][6], o[j][7]);
@@ -465,8 +477,7 @@ __global__ void __launch_bounds__(PairCfg<FP8, SPARSE>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int j = 2 * i + (lane >> 4);
-        e4m3x16_to_bf16x16(cur.far[i], __shfl_sync(0xffffffffu, cur.far_scale, 2 * j + ((lane >> 3) & 1)), o[i]);
-        const uint4 lo = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]), hi = make_uint4(o[i][4], o[i][5], o[i][6], o[i][7]);
+        const uint4 lo = make_uint4(of[i][0], of[i][1], of[i][2], of[i][3]), hi = make_uint4(of[i][4], of[i][5], of[i][6], of[i][7]);
         const int row = 32 - 32 * rank + r0 + j;
         st_shared_v4(dst + sw128_offset(row, 2 * wch + odd), odd ? hi : lo);
         st_shared_v4(dst + sw128_offset(row, 2 * wch + 1 - odd), odd ? lo : hi);
