@@ -268,8 +268,8 @@ constexpr int kLatentTile = 64;  // keys of a tile
 // Query rows of a CTA, and whether two CTAs of 64 work as a pair. Up to 32 rows
 // a block of 64 would multiply as many rows of zeros. Above, 32 sequences x 128
 // rows of up to 8192 keys took 142 us (bf16 pages) and 207 us (e4m3) in blocks of
-// 32, each of which copies or widens every tile again; now 103 and 135 us in blocks
-// of 64 and 90 and 128 us in pairs (2048 selected rows a query: 60 and 56 us).
+// 32, each of which copies or widens every tile again; now 100 and 114 us in blocks
+// of 64 and 89 and 102 us in pairs (2048 selected rows a query: 53 and 49 us).
 inline int latent_block(int64_t rows) { return rows <= 32 ? 32 : 64; }
 inline bool latent_pair(int64_t rows) { return rows > 64; }
 

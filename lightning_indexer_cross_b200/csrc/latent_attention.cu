@@ -189,143 +189,148 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
   };
   const int br = a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;  // rows of a TMA box
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ tiles
-    find_tiles<FP8, SPARSE, kInfo>(a, len0, group, FP8 ? 16 : br, -1, infos, places, info_full, info_free, wait);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S = Q . K^T
-    constexpr uint32_t idesc = idesc_bf16_f32(M, kT, false, false);
-    const uint32_t ka = smem_u32(smem);
-    int pieces = 0, n = 0;  // stages used so far
+  // (One branch for each four warps: in a chain of single warps' the compiler spills
+  // in the softmax, whose reloads past the L1 that 227 KB leave cost a quarter of the
+  // e4m3 batch's time.)
+  if (warp < 4) {
+    if (warp == 0) {
+      // ------------------------------------------------------------ tiles
+      find_tiles<FP8, SPARSE, kInfo>(a, len0, group, FP8 ? 16 : br, -1, infos, places, info_full, info_free, wait);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ S = Q . K^T
+      constexpr uint32_t idesc = idesc_bf16_f32(M, kT, false, false);
+      const uint32_t ka = smem_u32(smem);
+      int pieces = 0, n = 0;  // stages used so far
 #pragma unroll 1
-    for (int t = 0;; ++t, ++n) {
-      TileInfo x;
-      if (!get_info(t, x) || (x.flags & kEnd)) break;
-      if (x.flags & kFirst) {
-        if (!kQStage) {
-          if (pieces > 0 && !wait(q_free, (pieces - 1) & 1)) break;
-          if (lane == 0) mbar_arrive_expect_tx(q_full, 9 * R::kQSlab);
-          __syncwarp();
-          copy_q(x.b, qs, q_full);
-        }
-        ++pieces;
-        if (!wait(q_full, (pieces - 1) & 1)) break;
-        if (kQStage) {
-          if (lane == 0) mbar_arrive(&freed[n % kStages]);
-          __syncwarp();
-          ++n;
-        }
-      }
-      // the logits of tile t - 2 have been read
-      if (t >= 2 && !wait(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
-      const int st = n % kStages;
-      if (!wait(&full[st], (n / kStages) & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tmem + kSCol + (t & 1) * kCols;
-        const uint64_t bd = sw128_desc(ka + st * kTile, 16, 1024), ad = sw128_desc(smem_u32(qs), 16, 1024);
-#pragma unroll 1
-        for (int c = 0; c < 9; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if constexpr (kQStage)
-              mma_ws_bf16_ts(d, tmem + kQCol + c * 32 + kk * 8, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
-            else
-              mma_ws_bf16_ss(d, ad + c * (R::kQSlab >> 4) + kk * 2, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
-          }
-        mma_commit(&s_full[t & 1]);
-        if (x.flags & kLast) mma_commit(q_free);
-      }
-      __syncwarp();
-    }
-    // every MMA issued has retired before TMEM is released (the lane that
-    // elect_one names is the same each time)
-    if (elect_one()) mma_commit(retire);
-    __syncwarp();
-    mbar_drain(retire, 0);
-    if (!kQStage && pieces > 0) mbar_drain(q_full, (pieces - 1) & 1);  // given up: Q lands before the CTA exits
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P . V
-    constexpr uint32_t idesc = idesc_bf16_f32(M, 256, false, true);
-    const uint32_t va = smem_u32(smem), pa = smem_u32(ps);
-    int pieces = 0, nclear = 0, n = 0;
-#pragma unroll 1
-    for (int t = 0;; ++t, ++n) {
-      TileInfo x;
-      if (!get_info(t, x) || (x.flags & kEnd)) break;
-      const bool first = (x.flags & kFirst) != 0;
-      if (first) {
-        if (pieces > 0 && !wait(o_free, (pieces - 1) & 1)) break;
-        ++pieces;
-        if (kQStage) ++n;
-      }
-      if (!FP8 && (x.flags & kClear)) {
-        if (!wait(&cleared[nclear % kClears], (nclear / kClears) & 1)) break;
-        ++nclear;
-      }
-      const int st = n % kStages;
-      if (!wait(&full[st], (n / kStages) & 1)) break;
-      if (!wait(&p_ready[t & 1], (t >> 1) & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t vd = sw128_desc(va + st * kTile, kSlab, 1024), pd = sw128_desc(pa + (t % R::kPBufs) * R::kP, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_ws_bf16_ss(tmem + kOutCol + h * kDims, pd + kk * 2, vd + h * (4 * kSlab >> 4) + kk * 128, idesc,
-                           !first || kk > 0);
-        mma_commit(&freed[st]);
-        mma_commit(&pv_done[t & 1]);
-      }
-      __syncwarp();
-    }
-    if (elect_one()) mma_commit(retire);
-    __syncwarp();
-    mbar_drain(retire, 0);
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ copies (bf16)
-    // The stages have one producer that fills them in order: a second one that
-    // ran ahead would take the parity of an older phase for its own.
-    if (!FP8) {
-      int n = 0;
-      auto stage = [&](uint32_t bytes) {  // the next stage, ready for copies of so many bytes
-        if (!wait(&freed[n % kStages], ((n / kStages) & 1) ^ 1)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&full[n % kStages], bytes);
-        __syncwarp();
-        return true;
-      };
-      for (int t = 0;; ++t) {
+      for (int t = 0;; ++t, ++n) {
         TileInfo x;
         if (!get_info(t, x) || (x.flags & kEnd)) break;
-        if (kQStage && (x.flags & kFirst)) {
-          if (!stage(9 * R::kQSlab)) break;
-          copy_q(x.b, smem + (n % kStages) * kTile, &full[n % kStages]);
-          ++n;
-        }
-        if (!stage(kTile)) break;
-        // boxes without a valid row read the page behind the last, which fills zeros
-        if (elect_one()) {
-          uint8_t* dst = smem + (n % kStages) * kTile;
-          int py = x.row0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i * br >= kT) break;
-            const int pz = x.at[i] < 0 ? a.num_pages : static_cast<int>(x.at[i]);
-#pragma unroll
-            for (int c = 0; c < 9; ++c)
-              tma_load_3d(dst + c * kSlab + i * br * 128, &kvmap, &full[n % kStages], c * 64, py, pz);
-            py += br;
-            if (py >= a.page_size) py = 0;
+        if (x.flags & kFirst) {
+          if (!kQStage) {
+            if (pieces > 0 && !wait(q_free, (pieces - 1) & 1)) break;
+            if (lane == 0) mbar_arrive_expect_tx(q_full, 9 * R::kQSlab);
+            __syncwarp();
+            copy_q(x.b, qs, q_full);
+          }
+          ++pieces;
+          if (!wait(q_full, (pieces - 1) & 1)) break;
+          if (kQStage) {
+            if (lane == 0) mbar_arrive(&freed[n % kStages]);
+            __syncwarp();
+            ++n;
           }
         }
+        // the logits of tile t - 2 have been read
+        if (t >= 2 && !wait(&p_ready[t & 1], ((t >> 1) - 1) & 1)) break;
+        const int st = n % kStages;
+        if (!wait(&full[st], (n / kStages) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + kSCol + (t & 1) * kCols;
+          const uint64_t bd = sw128_desc(ka + st * kTile, 16, 1024), ad = sw128_desc(smem_u32(qs), 16, 1024);
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if constexpr (kQStage)
+                mma_ws_bf16_ts(d, tmem + kQCol + c * 32 + kk * 8, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
+              else
+                mma_ws_bf16_ss(d, ad + c * (R::kQSlab >> 4) + kk * 2, bd + c * (kSlab >> 4) + kk * 2, idesc, c + kk > 0);
+            }
+          mma_commit(&s_full[t & 1]);
+          if (x.flags & kLast) mma_commit(q_free);
+        }
         __syncwarp();
-        ++n;
       }
-      // the last copies of each stage land before the CTA exits, whatever their readers do
-      for (int u = n > kStages ? n - kStages : 0; u < n; ++u)
-        if (lane == 0) mbar_drain(&full[u % kStages], (u / kStages) & 1);
+      // every MMA issued has retired before TMEM is released (the lane that
+      // elect_one names is the same each time)
+      if (elect_one()) mma_commit(retire);
       __syncwarp();
+      mbar_drain(retire, 0);
+      if (!kQStage && pieces > 0) mbar_drain(q_full, (pieces - 1) & 1);  // given up: Q lands before the CTA exits
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ O += P . V
+      constexpr uint32_t idesc = idesc_bf16_f32(M, 256, false, true);
+      const uint32_t va = smem_u32(smem), pa = smem_u32(ps);
+      int pieces = 0, nclear = 0, n = 0;
+#pragma unroll 1
+      for (int t = 0;; ++t, ++n) {
+        TileInfo x;
+        if (!get_info(t, x) || (x.flags & kEnd)) break;
+        const bool first = (x.flags & kFirst) != 0;
+        if (first) {
+          if (pieces > 0 && !wait(o_free, (pieces - 1) & 1)) break;
+          ++pieces;
+          if (kQStage) ++n;
+        }
+        if (!FP8 && (x.flags & kClear)) {
+          if (!wait(&cleared[nclear % kClears], (nclear / kClears) & 1)) break;
+          ++nclear;
+        }
+        const int st = n % kStages;
+        if (!wait(&full[st], (n / kStages) & 1)) break;
+        if (!wait(&p_ready[t & 1], (t >> 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = sw128_desc(va + st * kTile, kSlab, 1024), pd = sw128_desc(pa + (t % R::kPBufs) * R::kP, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_ws_bf16_ss(tmem + kOutCol + h * kDims, pd + kk * 2, vd + h * (4 * kSlab >> 4) + kk * 128, idesc,
+                             !first || kk > 0);
+          mma_commit(&freed[st]);
+          mma_commit(&pv_done[t & 1]);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit(retire);
+      __syncwarp();
+      mbar_drain(retire, 0);
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ copies (bf16)
+      // The stages have one producer that fills them in order: a second one that
+      // ran ahead would take the parity of an older phase for its own.
+      if (!FP8) {
+        int n = 0;
+        auto stage = [&](uint32_t bytes) {  // the next stage, ready for copies of so many bytes
+          if (!wait(&freed[n % kStages], ((n / kStages) & 1) ^ 1)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&full[n % kStages], bytes);
+          __syncwarp();
+          return true;
+        };
+        for (int t = 0;; ++t) {
+          TileInfo x;
+          if (!get_info(t, x) || (x.flags & kEnd)) break;
+          if (kQStage && (x.flags & kFirst)) {
+            if (!stage(9 * R::kQSlab)) break;
+            copy_q(x.b, smem + (n % kStages) * kTile, &full[n % kStages]);
+            ++n;
+          }
+          if (!stage(kTile)) break;
+          // boxes without a valid row read the page behind the last, which fills zeros
+          if (elect_one()) {
+            uint8_t* dst = smem + (n % kStages) * kTile;
+            int py = x.row0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i * br >= kT) break;
+              const int pz = x.at[i] < 0 ? a.num_pages : static_cast<int>(x.at[i]);
+#pragma unroll
+              for (int c = 0; c < 9; ++c)
+                tma_load_3d(dst + c * kSlab + i * br * 128, &kvmap, &full[n % kStages], c * 64, py, pz);
+              py += br;
+              if (py >= a.page_size) py = 0;
+            }
+          }
+          __syncwarp();
+          ++n;
+        }
+        // the last copies of each stage land before the CTA exits, whatever their readers do
+        for (int u = n > kStages ? n - kStages : 0; u < n; ++u)
+          if (lane == 0) mbar_drain(&full[u % kStages], (u / kStages) & 1);
+        __syncwarp();
+      }
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ Q, softmax and output
@@ -406,23 +411,27 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
       float scale;         // lane l < 16: group l & 3 of row l >> 2
     } u0, u1;
     const int odd = (lane >> 2) & 1, wch = lane & 3;
-    TileInfo x;  // of the tile that is loaded
-    int ring = 0;  // its descriptor slot
+    // of the tile that is loaded: its descriptor's slot, and what this warp needs of it
+    int ring = 0, b = 0;
+    bool more = false, first = true;
+    uint32_t valid = 0;
+    const uint8_t* rows = a.cache;  // dense: the first of the warp's
     auto fetch = [&](int t) {
       ring = t % kInfo;
       if (!wait(&info_full[ring], (t / kInfo) & 1)) return false;
-      x = infos[ring];
+      const TileInfo& x = infos[ring];
+      more = !(x.flags & kEnd);
+      first = (x.flags & kFirst) != 0;
+      b = x.b;
+      valid = x.mask[w >> 2] >> (8 * (w & 3));
+      if constexpr (!SPARSE) rows = a.cache + x.at[w >> 1] + (w & 1) * 8 * kLatentRowFp8;
       return true;
     };
-    auto load = [&](Unit& v, int h) {  // rows 8 w + 4 h + [0, 4) of x's tile
-      const int r0 = 8 * w + 4 * h;
-      const uint32_t m = (w & 4 ? x.mask[1] : x.mask[0]) >> (r0 & 31);
-      const uint8_t* base = a.cache;  // dense: the first of the four rows
-      if constexpr (!SPARSE)
-        base += (w & 4 ? (w & 2 ? x.at[3] : x.at[2]) : (w & 2 ? x.at[1] : x.at[0])) + (r0 & 15) * kLatentRowFp8;
+    auto load = [&](Unit& v, int h) {  // four of the warp's rows
+      const uint32_t m = valid >> (4 * h);
       auto row_of = [&](int j) -> const uint8_t* {
-        if constexpr (SPARSE) return a.cache + places[ring * kT + r0 + j];
-        else return base + j * kLatentRowFp8;
+        if constexpr (SPARSE) return a.cache + places[ring * kT + 8 * w + 4 * h + j];
+        else return rows + (4 * h + j) * kLatentRowFp8;
       };
       v.scale = 1.f;
       v.rot = make_uint4(0, 0, 0, 0);
@@ -435,8 +444,7 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
       if ((m >> (lane >> 3)) & 1u) v.rot = ld_nc_v4(row_of(lane >> 3) + 528 + (lane & 7) * 16);
     };
     uint32_t tile = 0;
-    int n = 0, b = 0, qn = -1;  // qn: stage of the last Q that this warp has copied
-    bool more = false, first = true;
+    int n = 0, qn = -1;  // qn: stage of the last Q that this warp has copied
     // widens one unit into the tile in stage n; once its registers are read,
     // `then` asks for what they hold next
     auto widen = [&](Unit& v, int h, auto&& then) {
@@ -466,17 +474,13 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
       return true;
     };
     bool ok = fetch(0);
-    if (ok) {
-      more = !(x.flags & kEnd);
-      b = x.b;
-      if (more) {
-        load(u0, 0);
-        load(u1, 1);
-        warp_arrive(&info_free[ring]);
-      }
+    if (ok && more) {
+      load(u0, 0);
+      load(u1, 1);
+      warp_arrive(&info_free[ring]);
     }
 #pragma unroll 1
-    for (int t = 0; more; ++t) {
+    for (int t = 0; ok && more; ++t) {
       // Every warp waits for every stage, Q's too, which the first of them
       // copies: a warp that skipped one could be two phases ahead at its next
       // wait, and take an older phase of the same parity for its own.
@@ -498,9 +502,6 @@ __global__ void __launch_bounds__(Cfg<FP8, SPARSE, M>::kThreads, 1)
       tile = smem_u32(smem) + (n % kStages) * kTile;
       ok = widen(u0, 0, [&] {
         if (!fetch(t + 1)) return false;
-        more = !(x.flags & kEnd);
-        first = (x.flags & kFirst) != 0;
-        b = x.b;
         if (more) load(u0, 0);
         return true;
       });
