@@ -595,3 +595,31 @@ def test_a_wait_that_gives_up_is_recorded_and_the_next_call_is_right(ops, fp8, H
     out, lse = ops.latent_decode(q, cache, table, ln, workspace=ws)
     assert status_of(ops, ws) == 0
     check_attention(out, lse, L.decode(q, cache, table, lens), max(lens))
+
+
+@pytest.mark.parametrize("H", [7, 40, 128])
+def test_every_row_of_a_tile_is_widened_in_every_block_size(ops, H):
+    """Queries of zeros weigh all rows alike, by exactly 1: the output is the mean of the rows, here of every code and
+    of scales that are no powers of two beside such. n sums in 32 bits, each off by 2^-22 of the terms' magnitudes at
+    most, and a division."""
+    g = gen(H)
+    n, page = 104, 16  # two tiles, the second ragged
+    pages = n // page + 1
+    cache = ops.new_latent_cache(pages, page, True)
+    codes = torch.randint(0, 256, (pages, page, 512), generator=g, device="cuda").to(torch.uint8)
+    codes[codes & 0x7f == 0x7f] = 0  # NaN
+    cache[..., :512] = codes
+    scales = torch.rand(pages, page, 4, generator=g, device="cuda") + 0.1
+    scales[:, ::2] = 2.0 ** torch.randint(-3, 4, (pages, page // 2, 4), generator=g, device="cuda")
+    cache[..., 512:528] = scales.view(torch.uint8)
+    perm = torch.randperm(pages, generator=g, device="cuda").int()
+    rows = torch.from_numpy(L.cache_rows(cache).astype(np.float32)).to(torch.bfloat16)  # [pages * page, 576]
+    slots = (perm.long()[:, None] * page + torch.arange(page, device="cuda")).reshape(-1)[:n]
+    v = f64(rows.reshape(-1, 576)[slots.cpu()])[:, :512]
+    lim = np.abs(v).mean(0) * (n * 2.0 ** -22 + 2.0 ** -20)
+    q = torch.zeros(2, H, 576, dtype=torch.bfloat16, device="cuda")
+    dense, _ = ops.latent_decode(q, cache, perm[None].repeat(2, 1), torch.tensor([n, n], device="cuda"),
+                                 out_dtype=torch.float32)
+    sparse, _ = ops.latent_sparse_decode(q, cache, slots.int()[None].repeat(2, 1).contiguous(), out_dtype=torch.float32)
+    for out in (dense, sparse):
+        assert np.all(np.abs(f64(out) - v.mean(0)) <= lim)
