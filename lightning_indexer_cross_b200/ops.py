@@ -475,13 +475,16 @@ def latent_sparse_decode(q: torch.Tensor, cache: torch.Tensor, slots: torch.Tens
 
 def slots_of(idx: torch.Tensor, block_table: torch.Tensor, page_size: int) -> torch.Tensor:
     """Positions idx [B, k] (int32, -1 padding; a top-k's output) as slots of a paged cache. A position past its row
-    of block_table, or of a page below 0, becomes slot 2^31 - 1, which no cache has: the attention records it."""
+    of block_table, of a page below 0, or whose slot is no int32, becomes slot 2^31 - 1, which no cache has: the
+    attention records it."""
     _need(idx.dim() == 2 and block_table.dim() == 2 and idx.shape[0] == block_table.shape[0], "idx [B, k], block_table [B, width]")
-    rows = min(block_table.shape[1] * page_size, 2 ** 31 - 1)
+    none = 2 ** 31 - 1
+    rows = min(block_table.shape[1] * page_size, none)
     _need(rows >= 1, "block_table has a column")
     p = idx.clamp(0, rows - 1)
-    page = torch.gather(block_table, 1, (p // page_size).long())
-    slot = torch.where((idx < rows) & (page >= 0), page * page_size + p % page_size, 2 ** 31 - 1)
+    page = torch.gather(block_table, 1, (p // page_size).long()).long()
+    slot = page * page_size + p % page_size  # 64 bits: an entry too large would wrap to another page's slot
+    slot = torch.where((idx < rows) & (page >= 0) & (slot < none), slot, none)
     return torch.where(idx >= 0, slot, idx).to(torch.int32)
 
 

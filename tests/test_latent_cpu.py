@@ -250,3 +250,18 @@ def test_slots_of_gives_no_cached_slot_past_the_table_or_for_pages_below_zero(op
     assert ops.slots_of(idx, table, 16).tolist() == [[127, none, none, none, none, -1]]
     with pytest.raises(ValueError):
         ops.slots_of(idx, table[:, :0], 16)
+
+
+def test_slots_of_gives_no_cached_slot_for_pages_whose_slots_pass_32_bits(ops):
+    """page * page_size + row is formed in 64 bits: an entry of the table that is too large becomes the slot that no
+    cache has, never a slot of another page and never the padding -1."""
+    none = 2 ** 31 - 1
+    table = torch.tensor([[2 ** 25, 2 ** 26, 2 ** 26 + 3, 2 ** 26 - 1, 2 ** 31 - 1, 5]], dtype=torch.int32)
+    idx = torch.tensor([[0, 63, 64, 127, 128, 129, 192, 255, 256, 319, 320, 383, -1]], dtype=torch.int32)
+    got = ops.slots_of(idx, table, 64)
+    assert got.dtype == torch.int32
+    assert got.tolist() == [[none] * 10 + [320, 383, -1]]
+    # the last page whose slots are all below it
+    last = torch.tensor([[2 ** 25 - 2]], dtype=torch.int32)
+    assert ops.slots_of(torch.tensor([[0, 63]], dtype=torch.int32), last, 64).tolist() == [[2 ** 31 - 128, 2 ** 31 - 65]]
+    assert ops.slots_of(idx[:, :1], torch.tensor([[2 ** 28 + 3]], dtype=torch.int32), 16).tolist() == [[none]]
