@@ -356,9 +356,10 @@ ic_status_t ic_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride
  *   pos, freq [32], mscale, layout: the rotary dims are rotated as by ic_rope;
  *          pos and freq NULL: stored as given.
  *   e4m3 rows: scale = 2^e, the least power of two >= max|y| / 448 over the
- *   128 dims, e >= -100 (1 if all are zero); code = e4m3(y / scale), to
- *   nearest even. An infinite y takes no part in the maximum and is stored as
- *   +-448 scale, a NaN as NaN. A reader's code * scale is exact in bf16.
+ *   128 dims, -100 <= e <= 119 (1 if all are zero); code = e4m3(y / scale),
+ *   to nearest even, at most +-448: an infinite y, which takes no part in the
+ *   maximum, and y beyond 448 * 2^119 are stored as +-448 scale; a NaN as NaN.
+ *   A reader's code * scale is finite and exact in bf16.
  *
  * ic_latent_read copies sequences back as bf16: rows cu_len[b] + p of out
  * [R, 576] are row p of sequence b, p < cu_len[b + 1] - cu_len[b] (e4m3 rows

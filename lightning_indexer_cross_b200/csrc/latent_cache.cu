@@ -6,11 +6,13 @@
 //   [512, 528) four fp32 scales, one for each 128 dims
 //   [528, 656) the 64 rotary values in bf16
 // value = code * scale with scale = 2^e, the least power of two that is at
-// least max|y| / 448 over the 128 dims (1 where all are zero, e >= -100). With
-// a power of two the division by the scale is exact, and so is the decoded
-// value in bf16 (4 significant bits): the only rounding is that of y / scale
-// to e4m3 (nearest even, at most half a step, 2^-4 of the value), and a reader
-// may form the products of a row in bf16 without a second one.
+// least max|y| / 448 over the 128 dims (1 where all are zero), -100 <= e <= 119.
+// With a power of two the division by the scale is exact, and so is the decoded
+// value in bf16 (4 significant bits, 448 * 2^119 at most; 256 * 2^120 would be
+// infinite): the only rounding is that of y / scale to e4m3 (nearest even, at
+// most half a step: 2^-4 |y|, or 2^-10 scale below 2^-6 scale), and a reader may
+// form the products of a row in bf16 without a second one. Values above 448 *
+// 2^119 = 1.75 * 2^127, in the last binade of bf16, are stored as that.
 //
 // Both kernels move each byte once with whole-line accesses, one warp a token,
 // and are bound by HBM for long runs (read-back of 82K e4m3 rows: 27 us, 5.4 TB/s
@@ -90,12 +92,12 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       // amax = m 2^E with m in [1, 2); 448 = 1.75 2^8: the least e with
-      // 2^e >= amax / 448 is E - 8, or E - 7 where m > 1.75
+      // 2^e >= amax / 448 is E - 8, or E - 7 where m > 1.75 (119 at most: see above)
       int e = 0;
       if (amax > 0.f) {
         const uint32_t bits = __float_as_uint(amax);  // a bf16 subnormal (E = -127 here) ends at e = -100 all the same
         e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = e < -100 ? -100 : e;
+        e = e < -100 ? -100 : e > 119 ? 119 : e;
       }
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, -e in [-119, 100]
       uint32_t c[2];

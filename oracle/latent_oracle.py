@@ -29,14 +29,14 @@ def rope(x, pos, freq, rot_off=0, layout="interleaved", mscale=1.0, transpose=Fa
 
 
 def pow2_scale(y):
-    """Least 2^e >= max|y| / 448 over the last axis (finite values), e >= -100; 1 where all are zero."""
+    """Least 2^e >= max|y| / 448 over the last axis (finite values), -100 <= e <= 119; 1 where all are zero."""
     y = _f64(y)
     amax = np.where(np.isfinite(y), np.abs(y), 0.0).max(axis=-1)
     s = np.ones_like(amax)
     for i in np.ndindex(amax.shape):
         if amax[i] > 0:
             e = -100
-            while 448.0 * 2.0 ** e < amax[i]:
+            while e < 119 and 448.0 * 2.0 ** e < amax[i]:
                 e += 1
             s[i] = 2.0 ** e
     return s

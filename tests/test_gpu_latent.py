@@ -623,3 +623,26 @@ def test_every_row_of_a_tile_is_widened_in_every_block_size(ops, H):
     sparse, _ = ops.latent_sparse_decode(q, cache, slots.int()[None].repeat(2, 1).contiguous(), out_dtype=torch.float32)
     for out in (dense, sparse):
         assert np.all(np.abs(f64(out) - v.mean(0)) <= lim)
+
+
+def test_the_largest_values_stay_finite(ops):
+    """Rows of the largest bf16, 255 * 2^120, alone, beside infinities and beside a NaN, and of the largest value that a
+    code reaches: scales of 2^119 at most, and a read-back that is finite and no further off than that."""
+    most = 448 * 2.0 ** 119
+    kv = torch.full((4, 576), 255 * 2.0 ** 120, dtype=torch.float64)
+    kv[1, 0], kv[1, 300] = float("inf"), float("-inf")
+    kv[1, 301] = -255 * 2.0 ** 120
+    kv[2, 5] = float("nan")
+    kv[3] = most
+    kv = kv.to(torch.bfloat16).cuda()
+    cache = ops.new_latent_cache(1, 16, True)
+    ws = ops.latent_append(kv, torch.arange(4, device="cuda"), cache)
+    assert status_of(ops, ws) == 0
+    assert np.all(f64(parts(cache[0, :4])[1]) == 2.0 ** 119)
+    out = torch.zeros(4, 576, dtype=torch.bfloat16, device="cuda")
+    ops.latent_read(cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([0, 4], device="cuda"), out)
+    want = np.full((4, 512), most)
+    want[1, 300] = want[1, 301] = -most
+    want[2, 5] = np.nan
+    assert np.array_equal(f64(out)[:, :512], want, equal_nan=True)
+    assert torch.equal(out[:, 512:], kv[:, 512:])

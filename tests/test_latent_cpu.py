@@ -265,3 +265,21 @@ def test_slots_of_gives_no_cached_slot_for_pages_whose_slots_pass_32_bits(ops):
     last = torch.tensor([[2 ** 25 - 2]], dtype=torch.int32)
     assert ops.slots_of(torch.tensor([[0, 63]], dtype=torch.int32), last, 64).tolist() == [[2 ** 31 - 128, 2 ** 31 - 65]]
     assert ops.slots_of(idx[:, :1], torch.tensor([[2 ** 28 + 3]], dtype=torch.int32), 16).tolist() == [[none]]
+
+
+def test_oracle_scale_keeps_every_code_finite_in_bf16():
+    """Up to the largest bf16, 255 * 2^120: a scale of 2^119 at most, as 256 * 2^120 = 2^128 would read back as
+    infinite; what 448 * 2^119 does not reach is stored as that."""
+    big = np.zeros((1, 576))
+    big[0, :512] = 255 * 2.0 ** 120
+    big[0, 1], big[0, 128] = np.inf, -np.inf
+    big[0, 256:384] = -448 * 2.0 ** 119
+    assert L.pow2_scale(big[:, :512].reshape(-1, 4, 128)).tolist() == [[2.0 ** 119] * 4]
+    codes, s = L.pack(big)
+    raw = np.zeros((1, 656), dtype=np.uint8)
+    raw[:, :512] = codes
+    raw[:, 512:528] = s.astype(np.float32).view(np.uint8)
+    back = torch.from_numpy(L.unpack(raw).astype(np.float32)).to(torch.bfloat16).double().numpy()
+    most = 448 * 2.0 ** 119
+    assert np.all(back[0, :128] == most) and back[0, 128] == -most and np.all(back[0, 129:256] == most)
+    assert np.all(back[0, 256:384] == -most) and np.all(back[0, 384:512] == most)
