@@ -1,13 +1,19 @@
-"""Build the C-ABI library ``libindexcache.so`` in-tree with nvcc for sm_100a.
+"""Build the C-ABI library ``libindexcache.so`` in-tree with nvcc for sm_100a,
+and ``_front.so``, the tensor front end of the paged latent cache, for the torch
+and the Python that run this.
 
 Usage: ``python -m lightning_indexer_cross_b200.build [--force]``. Objects go
-to ``_build/`` at the repository root; the shared library is written next to
-this file so the Python binding finds it.
+to ``_build/`` at the repository root; the shared libraries are written next to
+this file so the Python binding finds them. The library needs nvcc alone; where
+torch, Python's headers or a C++ compiler are missing it is built without the
+front end, and a line on stderr says so.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,6 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexcache.so")
 FRONT = os.path.join(PKG, "_front.so")
+FRONT_FOR = os.path.join(BUILD, "front.txt")  # the torch and the Python that FRONT is bound to
+FRONT_SOURCE = "front.cpp"
 SOURCES = ["api.cu", "indexer.cu", "topk.cu", "sparse_mla.cu", "topk_noalloc.cu", "append.cu", "gate.cu", "context_parallel.cu", "topk_threshold.cu", "overlap.cu",
            "rope.cu", "latent_cache.cu", "latent_attention.cu", "latent_pair.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -35,22 +43,63 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libindexcache.so")
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "indexcache.h"))
-    return files
+def _stale(target: str, sources) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in sources)
+
+
+def _header() -> str:
+    return os.path.join(INCLUDE, "indexcache.h")
+
+
+def lib_stale() -> bool:
+    return _stale(LIB, [_header()] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != FRONT_SOURCE])
+
+
+def front_missing() -> str:
+    """What the front end's build lacks here; empty if nothing."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    if shutil.which(_cxx()) is None:
+        return f"the C++ compiler {_cxx()}"
+    return ""
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _front_for() -> str:
+    """The torch and the Python of this process: an extension is bound to both."""
+    return f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+
+
+def front_stale() -> bool:
+    if _stale(FRONT, [_header(), os.path.join(CSRC, FRONT_SOURCE)]) or not os.path.exists(FRONT_FOR):
+        return True
+    with open(FRONT_FOR) as f:
+        return f.read() != _front_for()
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(FRONT):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FRONT))
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return lib_stale() or (not front_missing() and front_stale())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not needs_build():
-        return LIB
+    if force or lib_stale():
+        build_lib(verbose)
+    missing = front_missing()
+    if missing:
+        if not os.path.exists(FRONT):
+            print(f"_front.so is not built: {missing} is missing (ops.rope and ops.latent_* need it; libindexcache.so "
+                  "and the other operators do not)", file=sys.stderr)
+    elif force or front_stale():
+        build_front(nvcc())
+    return LIB
+
+
+def build_lib(verbose: bool = False) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
 
@@ -75,8 +124,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    build_front(cc)
-    return LIB
 
 
 def build_front(cc: str) -> None:
@@ -86,16 +133,19 @@ def build_front(cc: str) -> None:
     include = os.path.join(root, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
     lib = os.path.join(root, "lib")
+    os.makedirs(BUILD, exist_ok=True)
     tmp = FRONT + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-O2", "-std=c++17", "-Wall",
+    cmd = [_cxx(), "-shared", "-fPIC", "-O2", "-std=c++17", "-Wall", f'-DIC_TORCH_VERSION="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", include, "-isystem",
            os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
-           "-isystem", cuda, os.path.join(CSRC, "front.cpp"), "-o", tmp, "-L", PKG, "-l:libindexcache.so", "-L", lib,
+           "-isystem", cuda, os.path.join(CSRC, FRONT_SOURCE), "-o", tmp, "-L", PKG, "-l:libindexcache.so", "-L", lib,
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on front.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FRONT)
+    with open(FRONT_FOR, "w") as f:
+        f.write(_front_for())
 
 
 if __name__ == "__main__":

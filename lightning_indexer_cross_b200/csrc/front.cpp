@@ -338,4 +338,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_front", "Tensor front end of the 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__front() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__front() {
+  PyObject* m = PyModule_Create(&module);
+  // the tensors' layout is that torch's: ops.py calls nothing here under another
+  if (m && PyModule_AddStringConstant(m, "torch_version", IC_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -13,9 +13,33 @@ from typing import List, Optional, Sequence
 
 import torch
 
-from . import _abi, _front
+from . import _abi
 
-_front.set_error(_abi.ICError)
+
+class _NoFront:
+    """In the place of the front end's extension where there is none for this torch: its functions cannot be called,
+    the operators that go through ``_abi`` need none."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs the extension _front.so: {self._why}; build it with "
+                          "`python -m lightning_indexer_cross_b200.build` (there is no fallback implementation)")
+
+
+def _load_front():
+    try:
+        from . import _front
+    except ImportError as e:
+        return _NoFront(str(e))
+    if _front.torch_version != torch.__version__:
+        return _NoFront(f"it was built for torch {_front.torch_version}, this is {torch.__version__}")
+    _front.set_error(_abi.ICError)
+    return _front
+
+
+_front = _load_front()
 
 D_QK = 576
 D_V = 512
