@@ -936,7 +936,7 @@ ic_status_t ic_latent_append(const void* kv, int64_t kv_stride, const int64_t* s
   if (!kv || !slots || T < 1 || T >= (int64_t(1) << 31)) return IC_ERR_INVALID_ARG;
   if (cache_dtype != IC_BF16 && cache_dtype != IC_FP8_E4M3) return IC_ERR_UNSUPPORTED;
   if (!paged_cache_ok(cache, cache_dtype, num_pages, page_size, page_stride)) return IC_ERR_INVALID_ARG;
-  if (!aligned16(kv) || kv_stride < 0 || (T > 1 && kv_stride < 576) || kv_stride % 8 != 0) return IC_ERR_INVALID_ARG;
+  if (!aligned16(kv) || kv_stride < 0 || (T > 1 && (kv_stride < 576 || kv_stride % 8 != 0))) return IC_ERR_INVALID_ARG;
   if ((pos != nullptr) != (freq != nullptr)) return IC_ERR_INVALID_ARG;
   if (pos && ((layout != IC_ROPE_INTERLEAVED && layout != IC_ROPE_HALF) || !std::isfinite(mscale)))
     return IC_ERR_INVALID_ARG;

@@ -646,3 +646,20 @@ def test_the_largest_values_stay_finite(ops):
     want[2, 5] = np.nan
     assert np.array_equal(f64(out)[:, :512], want, equal_nan=True)
     assert torch.equal(out[:, 512:], kv[:, 512:])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_of_one_row_whatever_its_stride(ops, fp8):
+    """One token: the distance to a next row means nothing (a transposed column and a cut row have odd ones)."""
+    g = gen(14)
+    col = torch.randn(576, 1, generator=g, device="cuda").to(torch.bfloat16)
+    wide = torch.zeros(1, 579, dtype=torch.bfloat16, device="cuda")
+    wide[:, :576] = col.t()
+    slot = torch.tensor([7], device="cuda")
+    want = ops.new_latent_cache(1, 16, fp8)
+    ops.latent_append(col.t().contiguous().view(576).view(1, 576), slot, want)
+    assert want[0, 7].any()
+    for kv in (col.t(), wide[:, :576]):
+        cache = ops.new_latent_cache(1, 16, fp8)
+        assert status_of(ops, ops.latent_append(kv, slot, cache)) == 0
+        assert torch.equal(cache.view(torch.uint8), want.view(torch.uint8))
