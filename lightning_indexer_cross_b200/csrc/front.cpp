@@ -209,7 +209,7 @@ PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   NEED(out.dim() == 2 && out.size(1) == kDqk && out.scalar_type() == at::kBFloat16 && out.is_contiguous(),
        "out is bf16 [R, 576], dense");
   const c10::cuda::OptionalCUDAGuard guard(dev);
-  if (out.size(0) > 0) {
+  if (out.size(0) > 0 && t.rows > 0) {
     const at::Tensor ws = workspace_of(given, ic_latent_read_workspace_size(), dev);
     if (failed(ic_latent_read(c.data, c.dtype, c.pages, as_int(c.page_size), c.stride, t.data, t.stride, as_int(t.width),
                               data<int64_t>(cu), as_int(t.rows), out.data_ptr(), out.size(0), ws.data_ptr(), ws.numel(),

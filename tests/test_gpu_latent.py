@@ -663,3 +663,14 @@ def test_append_of_one_row_whatever_its_stride(ops, fp8):
         cache = ops.new_latent_cache(1, 16, fp8)
         assert status_of(ops, ops.latent_append(kv, slot, cache)) == 0
         assert torch.equal(cache.view(torch.uint8), want.view(torch.uint8))
+
+
+def test_read_of_an_empty_batch_leaves_every_row(ops):
+    """No sequences: as for the other calls there is nothing to do, and the rows of out stay as they are."""
+    cache = ops.new_latent_cache(2, 16, True)
+    out = torch.full((5, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    table, cu = torch.zeros(0, 3, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    assert ops.latent_read(cache, table, cu, out) is out
+    assert bool((out == 7).all())
+    o, s = ops.latent_decode(torch.zeros(0, 8, 576, dtype=torch.bfloat16, device="cuda"), cache, table, cu[:0])
+    assert o.shape == (0, 8, 512) and s.shape == (0, 8)
