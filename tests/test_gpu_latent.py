@@ -674,3 +674,49 @@ def test_read_of_an_empty_batch_leaves_every_row(ops):
     assert bool((out == 7).all())
     o, s = ops.latent_decode(torch.zeros(0, 8, 576, dtype=torch.bfloat16, device="cuda"), cache, table, cu[:0])
     assert o.shape == (0, 8, 512) and s.shape == (0, 8)
+
+
+# ---------------------------------------------------------------- the rotation's grid
+def rotated64(x, pos, freq, off, layout, mscale):
+    """(y, limit) in 64 bits on the GPU, from the formula; the limit is the one of this file's head, 0 for copied dims."""
+    n = freq.numel()
+    a = torch.arange(n, device="cuda") * (2 if layout == "interleaved" else 1) + off
+    b = a + (1 if layout == "interleaved" else n)
+    angle = pos.double()[:, None, None] * freq
+    c, s = mscale * angle.cos(), mscale * angle.sin()
+    y = x.double()
+    u, v = y[..., a], y[..., b]
+    lim = torch.zeros_like(y)
+    y[..., a], y[..., b] = u * c - v * s, u * s + v * c
+    for d in (a, b):
+        lim[..., d] = 2.0 ** -20 * mscale * (u.abs() + v.abs()) + U[x.dtype] * 1.001 * y[..., d].abs()
+    return y, lim
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("T,H,D,off,rot", [
+    (5, 128, 576, 512, 64),     # a decode step: blocks of 15 heads (fp32: 8), the last of 8
+    (300, 131, 64, 0, 64),      # blocks of heads in place too, the last of 3
+    (2401, 8, 576, 512, 64),    # two tokens a CTA, the last alone
+    (8192, 64, 128, 0, 64),     # a prompt: four tokens a CTA, copies in several turns
+    (4737, 128, 64, 0, 64),     # nothing copied: rotated words in several turns
+    (3, 2, 16384, 16, 1024),    # one head's copies in several turns
+    (40001, 1, 64, 0, 64),      # many tokens a CTA
+    (230, 300, 70, 1, 66),      # unaligned: blocks of heads, and more than one token a CTA
+])
+def test_rope_in_every_shape_of_its_grid(ops, dtype, layout, T, H, D, off, rot):
+    g = gen(T + H)
+    x = torch.randn(T, H, D, generator=g, device="cuda").to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda")
+    freq, _ = ops.rope_frequencies(rot)
+    want, lim = rotated64(x, pos, freq, off, layout, 1.25)
+    y = ops.rope(x, pos, freq, rot_off=off, layout=layout, mscale=1.25)
+    assert bool(((y.double() - want).abs() <= lim).all()), ((y.double() - want).abs() - lim).max().item()
+    del want, lim
+    w = x.clone()
+    ops.rope(w, pos, freq, rot_off=off, layout=layout, mscale=1.25, out=w)
+    assert torch.equal(w, y)
+    heads_first = torch.empty(H, T, D, dtype=dtype, device="cuda").transpose(0, 1)
+    ops.rope(x, pos, freq, rot_off=off, layout=layout, mscale=1.25, out=heads_first)
+    assert torch.equal(heads_first, y)
