@@ -720,3 +720,26 @@ def test_rope_in_every_shape_of_its_grid(ops, dtype, layout, T, H, D, off, rot):
     heads_first = torch.empty(H, T, D, dtype=dtype, device="cuda").transpose(0, 1)
     ops.rope(x, pos, freq, rot_off=off, layout=layout, mscale=1.25, out=heads_first)
     assert torch.equal(heads_first, y)
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_a_sparse_wait_that_gives_up_is_recorded_and_the_next_call_is_right(ops, H):
+    """The same for selected rows, in each block size: a ring of three descriptors, with the rows' places beside it."""
+    from lightning_indexer_cross_b200 import _abi
+    g = gen(15)
+    B, k, page = 3, 700, 64
+    cache = random_cache(ops, 40, page, True, g)
+    slots = torch.randint(0, 40 * page, (B, k), generator=g, device="cuda").int()
+    slots[1, 100:] = -1
+    q = queries((B, H), g)
+    ws = ops.new_workspace(ops.latent_sparse_workspace_size(B, H, k), "cuda")
+    default = _abi.ic_wait_limit_ns()
+    try:
+        _abi.ic_set_wait_limit_ns(0)
+        ops.latent_sparse_decode(q, cache, slots, workspace=ws)
+    finally:
+        _abi.ic_set_wait_limit_ns(default)
+    assert status_of(ops, ws) == _abi.IC_ERR_TIMEOUT
+    out, lse = ops.latent_sparse_decode(q, cache, slots, workspace=ws)
+    assert status_of(ops, ws) == 0
+    check_attention(out, lse, L.sparse(q, cache, slots), k)
