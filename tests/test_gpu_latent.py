@@ -743,3 +743,38 @@ def test_a_sparse_wait_that_gives_up_is_recorded_and_the_next_call_is_right(ops,
     out, lse = ops.latent_sparse_decode(q, cache, slots, workspace=ws)
     assert status_of(ops, ws) == 0
     check_attention(out, lse, L.sparse(q, cache, slots), k)
+
+
+@pytest.mark.parametrize("H", [16, 64, 96, 128])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "sparse"])
+def test_calls_repeat_bit_for_bit_whatever_runs_beside_them(ops, kind, H):
+    """Ragged sequences in each block size: right once, and then the same bits with a cold L2, a warm one, and a second
+    call on another stream at the same time. (What a CTA tells the other one of its pair, a wait too few would show.)"""
+    g = gen(16 + H)
+    lens, page, k = [4000, 1, 0, 65, 2111, 1024, 777, 3333, 130, 64, 4001, 5], 32, 1100
+    B = len(lens)
+    table, pages = paged(lens, page, g)
+    cache = random_cache(ops, pages, page, kind != "bf16", g)
+    q, sink = queries((B, H), g), torch.randn(H, generator=g, device="cuda")
+    gate = torch.randn(B, H, 512, generator=g, device="cuda").to(torch.bfloat16)
+    if kind == "sparse":
+        slots = torch.randint(0, pages * page, (B, k), generator=g, device="cuda").int()
+        slots[3, 700:] = -1
+        want = L.sparse(q, cache, slots, sink, gate)
+        call = lambda **kw: ops.latent_sparse_decode(q, cache, slots, sink=sink, gate=gate, **kw)  # noqa: E731
+    else:
+        ln = torch.tensor(lens, device="cuda")
+        want = tuple(x[:, 0] for x in L.decode(q[:, None], cache, table, lens, sink, gate[:, None]))
+        call = lambda **kw: ops.latent_decode(q, cache, table, ln, sink=sink, gate=gate, **kw)  # noqa: E731
+    out, lse = call()
+    check_attention(out, lse, want, max(lens))
+    side, big = torch.cuda.Stream(), torch.empty(64 << 20, dtype=torch.int32, device="cuda")
+    for i in range(30):
+        if i % 3 == 0:
+            big.fill_(i)  # past what L2 holds
+        side.wait_stream(torch.cuda.current_stream())
+        beside = call(stream=side) if i % 3 == 2 else None
+        got = call()
+        torch.cuda.current_stream().wait_stream(side)
+        for o, s in (got, beside or got):
+            assert torch.equal(o, out) and torch.equal(s, lse), i
