@@ -778,3 +778,56 @@ def test_calls_repeat_bit_for_bit_whatever_runs_beside_them(ops, kind, H):
         torch.cuda.current_stream().wait_stream(side)
         for o, s in (got, beside or got):
             assert torch.equal(o, out) and torch.equal(s, lse), i
+
+
+def test_the_bindings_functions_equal_the_tensor_front_end(ops):
+    """The C calls through _abi, on raw pointers, against the same calls on tensors: rotation, append, read-back, dense
+    and sparse attention, with every argument at a value of its own."""
+    from lightning_indexer_cross_b200 import _abi
+    g = gen(17)
+    B, Q, H, page, k, T = 2, 2, 5, 32, 40, 50
+    st = ops._stream_ptr()
+    P = ops._ptr
+    x = torch.randn(T, 3, 100, generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda")
+    freq, _ = ops.rope_frequencies(64)
+    y = torch.empty(3, T, 100, dtype=torch.bfloat16, device="cuda")
+    _abi.ic_rope(P(x), 300, 100, P(pos), P(freq), 1.5, _abi.IC_ROPE_HALF, 1, _abi.IC_BF16, T, 3, 100, 20, 64, P(y), 100,
+                 T * 100, st)
+    assert torch.equal(y.transpose(0, 1), ops.rope(x, pos, freq, rot_off=20, layout="half", mscale=1.5, transpose=True))
+    kv = torch.randn(T, 600, generator=g, device="cuda").to(torch.bfloat16)[:, :576]
+    slots = torch.randperm(3 * page, generator=g, device="cuda")[:T]
+    table = torch.tensor([[2, 0, 9], [1, 2, 0]], dtype=torch.int32, device="cuda")[:, :2]
+    lens, cu = torch.tensor([33, 60], device="cuda"), torch.tensor([0, 33, 93], device="cuda")
+    q, sink = queries((B, Q, H), g), torch.randn(H, generator=g, device="cuda")
+    gate = torch.randn(B, Q, H, 512, generator=g, device="cuda").to(torch.bfloat16)
+    sel = torch.randint(0, 3 * page, (B, k), generator=g, device="cuda").int()
+    ws = ops.new_workspace(max(_abi.ic_latent_decode_workspace_size(B, Q, H, 2 * page),
+                               _abi.ic_latent_sparse_workspace_size(B, H, k), _abi.ic_latent_append_workspace_size(),
+                               _abi.ic_latent_read_workspace_size()), "cuda")
+    n = ws.numel()
+    for fp8 in (False, True):
+        code = _abi.IC_FP8_E4M3 if fp8 else _abi.IC_BF16
+        big = [ops.new_latent_cache(4, page + 16, fp8) for _ in range(2)]
+        a, b = (c[:3, :page] for c in big)
+        stride = big[0].stride(0) * big[0].element_size()
+        ops.latent_append(kv, slots, a, pos=pos, freq=freq, layout="half", mscale=0.5)
+        _abi.ic_latent_append(P(kv), 600, P(slots), P(pos), P(freq), 0.5, _abi.IC_ROPE_HALF, T, code, P(b), 3, page, stride,
+                              P(ws), n, st)
+        assert torch.equal(big[0].view(torch.uint8), big[1].view(torch.uint8)) and a.any()
+        want = ops.latent_read(a, table, cu, torch.zeros(95, 576, dtype=torch.bfloat16, device="cuda"))
+        got = torch.zeros_like(want)
+        _abi.ic_latent_read(P(b), code, 3, page, stride, P(table), 3, 2, P(cu), B, P(got), 95, P(ws), n, st)
+        assert torch.equal(got, want) and want.any()
+        out, lse = ops.latent_decode(q, a, table, lens, sink=sink, gate=gate, sm_scale=0.07, out_dtype=torch.float32)
+        o, s = torch.empty_like(out), torch.empty_like(lse)
+        _abi.ic_latent_decode(P(q), P(b), code, 3, page, stride, P(table), 3, 2, P(lens), P(sink), P(gate), 0.07, B, Q, H,
+                              _abi.IC_F32, P(o), P(s), P(ws), n, st)
+        assert torch.equal(o, out) and torch.equal(s, lse)
+    out, lse = ops.latent_sparse_decode(q[:, 0].contiguous(), a, sel, sink=sink, gate=gate[:, 1].contiguous(), sm_scale=0.07)
+    o, s = torch.empty_like(out), torch.empty_like(lse)
+    q0, gate1 = q[:, 0].contiguous(), gate[:, 1].contiguous()
+    _abi.ic_latent_sparse_decode(P(q0), P(b), 3, page, stride, P(sel), k, P(sink), P(gate1), 0.07, B, H, _abi.IC_BF16, P(o),
+                                 P(s), P(ws), n, st)
+    assert torch.equal(o, out) and torch.equal(s, lse)
+    assert status_of(ops, ws) == 0

@@ -283,3 +283,31 @@ def test_oracle_scale_keeps_every_code_finite_in_bf16():
     most = 448 * 2.0 ** 119
     assert np.all(back[0, :128] == most) and back[0, 128] == -most and np.all(back[0, 129:256] == most)
     assert np.all(back[0, 256:384] == -most) and np.all(back[0, 384:512] == most)
+
+
+# ---------------------------------------------------------------- the binding's functions
+def test_the_bindings_functions_raise_on_refusals(abi):
+    """The five calls under the header's names: a null or bad argument is an ICError with its code."""
+    p, keep = _fake()
+    rope = [p, 512, 128, p, p, 1.0, 0, 0, abi.IC_BF16, 4, 4, 128, 64, 64, ctypes.c_void_p(p.value + 65536), 512, 128, None]
+    append = [p, 576, p, p, p, 1.0, 0, 4, abi.IC_FP8_E4M3, p, 2, 16, 656 * 16, p, 256, None]
+    read = [p, abi.IC_BF16, 2, 16, 1152 * 16, p, 4, 4, p, 2, p, 10, p, 256, None]
+    decode = [p, p, abi.IC_BF16, 4, 16, 1152 * 16, p, 4, 4, p, None, None, 0.04, 2, 1, 8, abi.IC_BF16, p, None, p,
+              abi.ic_latent_decode_workspace_size(2, 1, 8, 64), None]
+    sparse = [p, p, 4, 16, 656 * 16, p, 100, None, None, 0.04, 2, 8, abi.IC_BF16, p, None, p,
+              abi.ic_latent_sparse_workspace_size(2, 8, 100), None]
+    for call, args, ws in ((abi.ic_rope, rope, None), (abi.ic_latent_append, append, -2), (abi.ic_latent_read, read, -2),
+                           (abi.ic_latent_decode, decode, -2), (abi.ic_latent_sparse_decode, sparse, -2)):
+        bad = [(0, None)] + ([(ws, 8)] if ws else [(5, float("nan"))])
+        for i, v in bad:
+            with pytest.raises(abi.ICError) as e:
+                call(*(args[:i] + [v] + args[i:][1:]))
+            assert e.value.code == abi.IC_ERR_INVALID_ARG and call.__name__ in str(e.value)
+    for call, args, i in ((abi.ic_rope, rope, 8), (abi.ic_latent_append, append, 8), (abi.ic_latent_read, read, 1),
+                          (abi.ic_latent_decode, decode, 2)):
+        with pytest.raises(abi.ICError) as e:
+            call(*(args[:i] + [7] + args[i + 1:]))
+        assert e.value.code == abi.IC_ERR_UNSUPPORTED
+    with pytest.raises(abi.ICError) as e:
+        abi.ic_latent_sparse_decode(*(sparse[:12] + [7] + sparse[13:]))
+    assert e.value.code == abi.IC_ERR_UNSUPPORTED
