@@ -44,8 +44,12 @@ IC_DEV uint32_t smem_u32(const void* p) {
 // programmatic serialisation) be scheduled while this one runs; pdl_wait
 // blocks until the previous kernel of the stream has completed and its
 // memory is visible. Every kernel of this library calls pdl_wait before its
-// first global-memory access and before allocating tensor memory. Both are
-// no-ops for kernels launched without the attribute.
+// first global-memory access and before allocating tensor memory, but for
+// latent_join_kernel, which reads inputs of its call (lengths, gate, sink) before
+// it: nothing in the stream can still be writing them, since the kernel before it,
+// the call's own, is launched without the attribute and starts only when all
+// earlier work is done. Both are no-ops for kernels launched without the
+// attribute.
 IC_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 IC_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -35,8 +35,9 @@ inline cudaError_t set_smem_once(Kernel kern, int bytes, bool (&done)[64]) {
 
 // Launch a kernel; with pdl set, with programmatic stream serialisation, so
 // it may start while the previous kernel in the stream (one of this library's,
-// which all wait with griddepcontrol.wait before touching global memory)
-// finishes. Only set pdl when the previous stream operation is such a kernel.
+// which wait with griddepcontrol.wait before touching global memory: see pdl_wait
+// for the one that reads earlier) finishes. Only set pdl when the previous stream
+// operation is such a kernel.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                  bool pdl, Args&&... args) {

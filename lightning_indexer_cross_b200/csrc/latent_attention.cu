@@ -550,8 +550,9 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
   const int row = rest / kCtas * 32 + lane;
   const int dim = (rest % kCtas * kPerCta + warp / WPP) * 16;
   pdl_trigger();
-  // tiles of all sequences, and of those before b. (The lengths were there before
-  // the main kernel started, so they are read before it ends.)
+  // tiles of all sequences, and of those before b. (The lengths, the gate and the
+  // sink were there before the main kernel started, which had no early start, so
+  // they are read before it ends.)
   int64_t total = 0, start = 0;
   int bt;
   if (SPARSE) {
@@ -700,6 +701,9 @@ cudaError_t launch_one(const CUtensorMap& qmap, const CUtensorMap& kvmap, const 
   static bool done[64] = {false};
   const cudaError_t e = set_smem_once(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
+  // no early start here: the joining kernel, which has it, reads the call's inputs
+  // before this one ends, and they are complete only because this one waited for
+  // everything before it
   return launch_kernel(kern, dim3(static_cast<unsigned>(a.groups) * a.rblocks), dim3(C::kThreads), C::kSmemBytes, stream,
                        false, qmap, kvmap, a);
 }

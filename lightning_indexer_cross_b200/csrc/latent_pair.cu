@@ -521,6 +521,7 @@ cudaError_t launch_pair(const CUtensorMap& qmap, const CUtensorMap& kvmap, const
   static bool done[64] = {false};
   const cudaError_t e = set_smem_once(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
+  // no early start: the joining kernel relies on it (launch_one in latent_attention.cu)
   return launch_kernel_cluster(kern, dim3(static_cast<unsigned>(a.groups) * a.rblocks), dim3(C::kThreads), C::kSmemBytes,
                                stream, false, 2, qmap, kvmap, a);
 }
