@@ -831,3 +831,50 @@ def test_the_bindings_functions_equal_the_tensor_front_end(ops):
                                  P(s), P(ws), n, st)
     assert torch.equal(o, out) and torch.equal(s, lse)
     assert status_of(ops, ws) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H", [9, 48, 100])
+def test_decode_from_spaced_pages_and_a_cut_table(ops, fp8, H):
+    """Pages some rows apart, a block table that is a part of a wider one, an odd page size, NaN in every row that holds
+    no token."""
+    g = gen(18)
+    lens, Q, page = [333, 0, 81, 5], 2, 80
+    need = [-(-n // page) for n in lens]
+    big = ops.new_latent_cache(sum(need) + 1, page + 8, fp8)
+    big.view(torch.uint8).fill_(0xff)
+    cache = big[:, :page]
+    wide = torch.full((len(lens), max(need) + 3), 1 << 30, dtype=torch.int32, device="cuda")
+    table = wide[:, :max(need)]
+    perm = torch.randperm(sum(need) + 1, generator=g, device="cuda").int()
+    at = 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = perm[at:at + need[b]]
+        at += need[b]
+        p = torch.arange(n, device="cuda")
+        if n:
+            kv = torch.randn(n, 576, generator=g, device="cuda").to(torch.bfloat16)
+            ops.latent_append(kv, table[b].long()[p // page] * page + p % page, cache)
+    q = queries((len(lens), Q, H), g)
+    ws = ops.new_workspace(ops.latent_decode_workspace_size(len(lens), Q, H, table.shape[1] * page), "cuda")
+    ws[256:] = 0xff  # partial results that nothing has written are NaN
+    out, lse = ops.latent_decode(q, cache, table, torch.tensor(lens, device="cuda"), workspace=ws, out_dtype=torch.float32)
+    assert status_of(ops, ws) == 0
+    with np.errstate(invalid="ignore"):
+        check_attention(out, lse, L.decode(q, cache, table, lens), max(lens))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shares_of_more_tiles_than_32_bits_divide(ops, fp8):
+    """4300 sequences of 65536 rows that share their pages: 4.4 million tiles, whose shares are counted in 64 bits."""
+    g = gen(19)
+    B, H, page, pages = 4300, 2, 128, 512
+    cache = random_cache(ops, pages, page, fp8, g)
+    table = torch.stack([torch.randperm(pages, generator=g, device="cuda").int() for _ in range(4)]).repeat(B // 4, 1)
+    q = queries((B, H), g)
+    lens = torch.full((B,), pages * page, device="cuda")
+    lens[3::11] -= 1
+    out, lse = ops.latent_decode(q, cache, table, lens, out_dtype=torch.float32)
+    some = [0, 3, 2147, B - 1]
+    want = L.decode(q[some][:, None], cache, table[some], lens[some].tolist())
+    check_attention(out[some], lse[some], tuple(x[:, 0] for x in want), pages * page)
