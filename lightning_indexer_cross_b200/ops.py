@@ -506,9 +506,10 @@ def slots_of(idx: torch.Tensor, block_table: torch.Tensor, page_size: int) -> to
     rows = min(block_table.shape[1] * page_size, none)
     _need(rows >= 1, "block_table has a column")
     p = idx.clamp(0, rows - 1)
-    page = torch.gather(block_table, 1, (p // page_size).long()).long()
-    slot = page * page_size + p % page_size  # 64 bits: an entry too large would wrap to another page's slot
-    slot = torch.where((idx < rows) & (page >= 0) & (slot < none), slot, none)
+    page = torch.gather(block_table, 1, (p // page_size).long())
+    # 64 bits, cut at none: in 32 a page number that is too large would wrap to another page's slot
+    slot = torch.add(p % page_size, page.long(), alpha=page_size).clamp(max=none)
+    slot = torch.where((idx < rows) & (page >= 0), slot, none)
     return torch.where(idx >= 0, slot, idx).to(torch.int32)
 
 
