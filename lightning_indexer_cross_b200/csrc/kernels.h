@@ -267,10 +267,18 @@ cudaError_t launch_latent_read(const LatentReadArgs& a, bool fp8, cudaStream_t s
 // ---------------------------------------------------------------- attention over the paged latent cache
 constexpr int kLatentTile = 64;  // keys of a tile
 // Query rows of a CTA, and whether two CTAs of 64 work as a pair. Up to 32 rows
-// a block of 64 would multiply as many rows of zeros. Above, 32 sequences x 128
-// rows of up to 8192 keys took 142 us (bf16 pages) and 207 us (e4m3) in blocks of
-// 32, each of which copies or widens every tile again; now 100 and 114 us in blocks
-// of 64 and 89 and 102 us in pairs (2048 selected rows a query: 53 and 49 us).
+// a block of 64 would multiply as many rows of zeros; above, every block of 32
+// copies or widens each tile again. us a call in blocks of 32 / of 64 / in pairs, no
+// gate, inputs in turn:
+//   rows                          32          33           64           65           96          128
+//   32 x up to 4096, bf16   45/50/49    46/55/50     47/56/51     58/56/51     59/56/51     72/60/55
+//   32 x up to 4096, e4m3   42/45/57    56/51/57     56/53/59     74/64/59     74/64/59     95/67/62
+//   4 x up to 32768, e4m3   33/37/43    39/37/43     40/39/45     51/46/45     51/46/45     61/47/45
+//   32 x 2048 selected      36/39/49    48/43/49     48/44/50     62/52/50     62/52/50     77/54/52
+//   1 x 512, bf16           12/13/14    12/13/14     12/13/14     12/14/14     12/14/14     12/14/14
+// The bounds are those of e4m3 pages. bf16 pages of 33 to 64 rows, copied by TMA
+// and not widened, would gain from two blocks of 32, and one short sequence of more
+// than 64 rows up to 2 us.
 inline int latent_block(int64_t rows) { return rows <= 32 ? 32 : 64; }
 inline bool latent_pair(int64_t rows) { return rows > 64; }
 

@@ -302,8 +302,11 @@ IC_DEV void softmax_rows(const LatentArgs& a, uint32_t tmem, uint8_t* ps, float*
 #pragma unroll
     for (int j = 0; j < kCols; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(rv[j]));
     offer(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-    // The sum is of the 32-bit weights; those of the product are rounded to
-    // bf16 (2^-8 of each at most, of either sign), as the MMA takes them.
+    // The sum is of the 32-bit weights; those of the product are rounded to bf16
+    // (2^-8 of each at most, of either sign), fp32 outputs too: kind::f16 takes
+    // both operands in one type, the values are bf16, and a second term of each
+    // weight would be as many MMAs again. (The error of bf16 outputs against 64
+    // bits is 1.6e-3 to 2.1e-3 of their norm so; their own rounding is 1.65e-3.)
     uint32_t pk[kCols / 2];
     float sum = 0.f;
     auto weigh = [&](float base) {

@@ -711,8 +711,12 @@ cudaError_t launch_one(const CUtensorMap& qmap, const CUtensorMap& kvmap, const 
 template <bool SPARSE, int M>
 cudaError_t launch_join(const LatentArgs& a, cudaStream_t stream) {
   // Pieces of a sequence: about groups / B + 1. More than four are shared by eight
-  // warps: 38 pieces of 4 sequences x 32 rows take 8 us so, 45 by one warp each; with
-  // three or four pieces both are within 0.5 us, and one warp needs no shared memory.
+  // warps. us a call of B sequences of e4m3 rows, 131072 in all, by one warp / eight:
+  //   B (pieces)    4        12       18       25       32       48
+  //   8 heads    68/31    41/33    42/39    39/38    39/41    37/44   (38, 13, 9, 6, 5, 4 pieces)
+  //   128 heads  67/45    55/60    60/71    57/74    63/82    62/95   (19, 7, 5, 3, 3, 2 pieces)
+  // With 128 heads, where eight warps are four times as many CTAs of a grid that is
+  // full already, the bound is 4 to 11 us on the wrong side at five to seven pieces.
   const bool many = a.groups / a.B + 1 > 4;
   const unsigned ctas = static_cast<unsigned>(a.B) * ((a.rows + 31) / 32) * (many ? 32 : 4);
   auto join = many ? latent_join_kernel<SPARSE, M, 8> : latent_join_kernel<SPARSE, M, 1>;

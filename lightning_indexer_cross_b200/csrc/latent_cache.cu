@@ -15,10 +15,10 @@
 // 2^119 = 1.75 * 2^127, in the last binade of bf16, are stored as that.
 //
 // Both kernels move each byte once with whole-line accesses, one warp a token,
-// and are bound by HBM for long runs (read-back of 82K e4m3 rows: 27 us, 5.4 TB/s
-// of 656 bytes read and 1152 written a row; 16384 rows appended: 8.3 us, 3.6 TB/s,
-// launch and the angles' latency among it) and by launch latency at decode sizes
-// (32 rows: 4 us).
+// and are bound by HBM for long runs (read-back of 82K e4m3 rows: 28.6 us a call,
+// 26.6 in a graph, 5.6 TB/s of 656 bytes read and 1152 written a row, bf16 rows 31.8;
+// 16384 rows appended, in a graph: e4m3 8.5 us, 3.5 TB/s, bf16 8.2, the angles'
+// latency among it) and by launch latency at decode sizes (32 rows in a graph: 2.3 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 // Output row r belongs to sequence b with cu[b] <= r < cu[b + 1]. A warp takes
 // kRows consecutive rows; lane j < kRows finds the place of row j, so that the
 // lookups of a warp are one chain: the sequence (32 probes a step, or none up to
-// 32 sequences), the page, the rows. 82K e4m3 rows: 27.4 us, 29.0 with 8 rows a
-// warp in two batches; 3 sequences of up to 1021 bf16 rows: 4.3 and 6.3 us.
+// 32 sequences), the page, the rows. Against 8 rows a warp in two batches, side by
+// side: 82K e4m3 rows 27.4 and 29.0 us, 3 sequences of up to 1021 bf16 rows 4.3 and
+// 6.3 us.
 constexpr int kRows = 4;
 
 template <bool FP8>

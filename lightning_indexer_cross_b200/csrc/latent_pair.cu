@@ -19,13 +19,20 @@
 // In each CTA lanes 0-63 of TMEM hold its 64 rows' first half of the columns,
 // lanes 64-127 the second, as in the single CTA's form.
 //
-// What bounds it. 32 ragged sequences of up to 8192 rows x 128 heads: 89 us from
-// bf16 pages, 102 from e4m3 (9 of them joining), where HBM would take 35 and 21 and
-// the MMAs 32. A tile's MMAs take 1250 cycles, its chain of softmax (logits read,
-// maxima exchanged between the halves, 2^x, weights stored and told to the first
-// CTA) and products 2300 (e4m3: 2700), and the next tile's logits are all that runs
-// beside it: a second buffer of weights and a second set of softmax warps would need
-// the memory of the values' second stage and registers that are not there.
+// What bounds it. 32 ragged sequences of up to 8192 rows x 128 heads: 97 us a call
+// from bf16 pages, 103 from e4m3, with inputs that change from call to call (87 and
+// 100 in a graph; 9 of them joining), where HBM would take 35 and 21 and the MMAs
+// 32. In the steady state a tile's MMAs take 1250 cycles, its chain of softmax
+// (logits read, maxima exchanged between the halves, 2^x, weights stored and told to
+// the first CTA) and products 2300 (e4m3: 2700), and the next tile's logits are all
+// that runs beside it. Starts and pieces come on top (2970 cycles a tile on average,
+// bf16): a share has 40 or 41 tiles in one to three pieces, and a further piece costs
+// 12500 cycles, as much as five tiles, since the pair drains at its end (the next Q
+// is copied after the last logits, the next product waits until the output has been
+// read out and written). The one share of three pieces ends 11 us after the average.
+// One buffer of weights: P(t) waits for the product of t - 1. A second (8 KB) would
+// fit in the 9 KB that are free; for bf16 pages the registers of a second softmax
+// warpgroup would be there too.
 //
 // Roles in each CTA. Warp 0 finds the tiles; warps 4-7 run the softmax and the
 // output; a warp loads Q. In the first CTA warps 1 and 2 issue the products of

@@ -13,8 +13,9 @@
 // once to the tensor's type.
 //
 // The step reads and writes every element once and computes little: it is
-// bound by HBM for long prompts (8192 x 64 x 128 bf16: 47 us, 5.7 TB/s, 0.87 of a
-// copy's rate) and by launch latency at decode sizes (32 x 128 x 576: 4.2 us). A CTA
+// bound by HBM for long prompts (8192 x 64 x 128, half layout, a call and in a graph:
+// bf16 48 and 46 us, 5.8 TB/s, 0.89 of a copy's rate; fp32 88 us in a graph, 6.1
+// TB/s) and by launch latency at decode sizes (32 x 128 x 576 bf16: 5.1 and 3.0 us). A CTA
 // takes `tpc` tokens x `hpc` heads: its threads first form the tokens' cosines
 // and sines in shared memory (once for all heads), then move 16-byte words,
 // kUnroll of them in flight a thread.
