@@ -71,8 +71,13 @@ def _cxx() -> str:
 
 
 def _front_for() -> str:
-    """The torch and the Python of this process: an extension is bound to both."""
-    return f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+    """The torch and the Python of this process: an extension is bound to both. (A torch that runs from its sources
+    names no version here; ops.py compares the one that the extension was compiled for.)"""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "from source"
+    return f"torch {version}, {sys.implementation.cache_tag}"
 
 
 def front_stale() -> bool:

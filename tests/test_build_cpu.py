@@ -94,3 +94,13 @@ def test_a_replaced_torch_or_python_rebuilds_the_front_extension_alone(fake_buil
     assert len(ran) == n + 1 and ran[-1][0] != "/fake/bin/nvcc" and not b.needs_build()
     os.remove(b.FRONT)
     assert b.needs_build()
+
+
+def test_a_torch_without_a_package_record_builds(fake_build, monkeypatch):
+    b, ran = fake_build
+
+    def version(name):
+        raise b.importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(b.importlib.metadata, "version", version)
+    assert b.build() == b.LIB and os.path.exists(b.FRONT) and not b.needs_build()
